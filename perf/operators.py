@@ -1,0 +1,482 @@
+"""What the bounded and int8 cache operators are measured on.
+
+Four operators of a paged KV cache, each in its plain form (elementary torch
+operations in 32 bits) and as the calls a serving program makes:
+
+* ``decode``  -- decode attention that also adds to every key's accumulated
+  attention weight (16-bit and int8 caches);
+* ``select``  -- the positions of each KV head that stay when a cache is cut
+  to a budget of keys by accumulated weight;
+* ``compact`` -- the kept rows moved to the front of their sequences, in place
+  (16-bit and int8 caches);
+* ``varlen``  -- packed prompt chunks and decode rows over an int8 cache.
+
+Shapes are those of the package's own workloads: 12/12 heads of 64, 32/8 heads
+of 128, blocks of 16 and 32 tokens.
+"""
+import math
+import random
+
+import numpy as np
+import torch
+
+own = False
+
+DT = {"f16": torch.float16, "bf16": torch.bfloat16}
+
+
+# ---- cases ---------------------------------------------------------------------
+
+def listed():
+    return [
+        # a handful of short chats on a small multi-head model: one call's latency
+        dict(name="decode tiny", op="decode", int8=False, dtype="f16", batch=4, hq=12, hkv=12, d=64, bs=16,
+             lo=16, hi=40, dist="uniform", window=0, seed=1),
+        # the serving batch of the package's headline: 256 sequences, grouped heads
+        dict(name="decode batch", op="decode", int8=False, dtype="f16", batch=256, hq=32, hkv=8, d=128, bs=16,
+             lo=512, hi=4096, dist="uniform", window=0, seed=2),
+        # a few documents of very different lengths, up to 128 k tokens
+        dict(name="decode skewed", op="decode", int8=False, dtype="bf16", batch=8, hq=32, hkv=8, d=128, bs=16,
+             lo=1024, hi=131072, dist="doubling", window=0, seed=3),
+        # the same batch work over a quantised cache
+        dict(name="decode int8", op="decode", int8=True, dtype="bf16", batch=64, hq=32, hkv=8, d=128, bs=32,
+             lo=512, hi=8192, dist="uniform", window=0, seed=4),
+        # eviction of the short chats: latency
+        dict(name="select tiny", op="select", batch=4, hkv=12, bs=16, lo=16, hi=40, dist="uniform", budget=24,
+             sink=2, recent=8, seed=5),
+        # one layer of the serving batch cut to 1,024 keys a head
+        dict(name="select batch", op="select", batch=256, hkv=8, bs=16, lo=512, hi=4096, dist="uniform",
+             budget=1024, sink=4, recent=128, seed=6),
+        # two long documents cut to 8,192 keys
+        dict(name="select long", op="select", batch=2, hkv=8, bs=16, lo=100001, hi=131072, dist="uniform",
+             budget=8192, sink=4, recent=1024, seed=7),
+        # the rows those selections move: short chats
+        dict(name="compact tiny", op="compact", int8=False, dtype="f16", batch=4, hkv=12, d=64, bs=16, lo=16, hi=40,
+             dist="uniform", budget=24, sink=2, recent=8, seed=8),
+        # one layer of a batch of longer chats halved
+        dict(name="compact batch", op="compact", int8=False, dtype="bf16", batch=64, hkv=8, d=128, bs=16, lo=2048,
+             hi=8192, dist="uniform", budget=2048, sink=4, recent=256, seed=9),
+        # a quantised cache: rows of differently scaled blocks meet in one block
+        dict(name="compact int8", op="compact", int8=True, dtype="f16", batch=32, hkv=8, d=128, bs=32, lo=1500,
+             hi=4096, dist="uniform", budget=1024, sink=4, recent=128, seed=10),
+        # a mixed step over a quantised cache: 16 prompt chunks of 512 rows behind 2,048 tokens, and 240 decode rows
+        dict(name="varlen mixed", op="varlen", dtype="f16", chunks=16, rows_lo=512, rows_hi=512, past_lo=2048,
+             past_hi=2048, batch=240, lo=256, hi=8192, hq=32, hkv=8, d=128, bs=32, causal=True, window=0, seed=11),
+        # the first chunks of three short prompts beside two decode rows
+        dict(name="varlen short", op="varlen", dtype="bf16", chunks=3, rows_lo=5, rows_hi=70, past_lo=0, past_hi=40,
+             batch=2, lo=20, hi=200, hq=32, hkv=8, d=128, bs=16, causal=True, window=0, seed=12),
+    ]
+
+
+def _log(rng, lo, hi):
+    return int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
+
+
+def draw(rng):
+    """A case of the same ranges: batches of 1 to 256, contexts of 1 to 131,072 tokens."""
+    op = rng.choice(["decode", "decode", "select", "compact", "varlen"])
+    seed = rng.randrange(1 << 30)
+    bs = rng.choice([16, 16, 32, 48, 64])
+    int8 = op == "varlen" or (op in ("decode", "compact") and rng.random() < 0.4)
+    if int8:
+        hkv, d = rng.choice([4, 8, 8]), 128
+    else:
+        hkv, d = rng.choice([(12, 64), (4, 64), (2, 128), (8, 128), (8, 128)])
+    group = rng.choice([1, 2, 4, 8] if hkv * d <= 768 else [1, 2, 4])
+    c = dict(op=op, dtype=rng.choice(["f16", "bf16"]), hq=hkv * group, hkv=hkv, d=d, bs=bs, seed=seed, dist="uniform")
+    if op == "varlen":
+        c.update(chunks=rng.randint(1, 8), rows_lo=2, rows_hi=_log(rng, 4, 900), past_lo=0, past_hi=_log(rng, 1, 2000),
+                 batch=rng.randint(0, 64), lo=1, hi=_log(rng, 8, 6000), causal=rng.random() < 0.8,
+                 window=rng.choice([0, 0, 0, _log(rng, 16, 1500)]))
+        return c
+    c["batch"] = _log(rng, 1, 256)
+    most = max(40, min(131072, 500000 // c["batch"]))       # tokens a sequence, so that a case stays below the largest
+    c["hi"] = _log(rng, 24, most)
+    c["lo"] = rng.randint(1, c["hi"])
+    if op == "decode":
+        c.update(int8=int8, window=rng.choice([0, 0, 0, rng.randint(1, c["hi"])]))
+        return c
+    c["budget"] = rng.randint(max(1, c["hi"] // 8), max(2, 3 * c["hi"] // 4))
+    c["sink"] = rng.choice([0, 0, 1, min(4, c["budget"] // 4)])
+    c["recent"] = rng.randint(0, c["budget"] // 2)
+    if op == "compact":
+        c["int8"] = int8
+    return c
+
+
+def _lengths(case):
+    rng = random.Random(case["seed"])
+    lo, hi, n = case["lo"], case["hi"], case["batch"]
+    if case["dist"] == "doubling":
+        return [min(hi, lo << i) for i in range(n)]
+    return [rng.randint(lo, hi) for _ in range(n)]
+
+
+def _rows(case):
+    """(query rows, keys) of every sequence of a packed step: the chunks, then the decode rows."""
+    rng = random.Random(case["seed"] + 1)
+    q, kv = [], []
+    for _ in range(case["chunks"]):
+        n = rng.randint(case["rows_lo"], case["rows_hi"])
+        q.append(n)
+        kv.append(n + rng.randint(case["past_lo"], case["past_hi"]))
+    for _ in range(case["batch"]):
+        q.append(1)
+        kv.append(rng.randint(case["lo"], case["hi"]))
+    return q, kv
+
+
+def work(case):
+    op, hkv = case["op"], case["hkv"]
+    if op == "varlen":
+        q, kv = _rows(case)
+        pairs = 0
+        keys = 0
+        for a, b in zip(q, kv):
+            first = b                                         # the lowest key that some row sees
+            for i in range(a):
+                last = b - a + i + 1 if case["causal"] else b
+                seen = min(last, case["window"]) if case["window"] else last
+                pairs += seen
+                first = min(first, last - seen)
+            keys += b - first
+        rows = sum(q) * case["hq"] * case["d"]
+        return {"bytes": 2 * keys * hkv * case["d"] + 2 * rows * 2, "flops": 4 * case["d"] * case["hq"] * pairs}
+    lens = _lengths(case)
+    if op == "decode":
+        keys = sum(min(L, case["window"]) if case["window"] else L for L in lens)
+        size = 1 if case["int8"] else 2
+        rows = len(lens) * case["hq"] * case["d"]
+        return {"bytes": 2 * keys * hkv * case["d"] * size + 2 * rows * 2 + 8 * keys * hkv,
+                "flops": 4 * keys * case["hq"] * case["d"]}
+    if op == "select":
+        return {"bytes": 4 * hkv * sum(L + min(L, case["budget"]) for L in lens), "flops": 0}
+    moved = 0
+    for L in lens:  # every kept row behind the sinks moves, but for the few ahead of the first key that goes
+        if L > case["budget"]:
+            moved += case["budget"] - case["sink"]
+    size = 1 if case["int8"] else 2
+    kept = sum(min(L, case["budget"]) for L in lens)
+    out = 2 * case["d"] * moved * hkv * size * 2 + 4 * hkv * kept + 8 * hkv * moved
+    if case["int8"]:  # the pools are read out as the values they stand for
+        blocks = sum(-(-L // case["bs"]) for L in lens)
+        out += 2 * blocks * case["bs"] * hkv * case["d"] * 5
+    return {"bytes": out, "flops": 0}
+
+
+# ---- inputs --------------------------------------------------------------------
+
+def _tables(lens, bs, gen):
+    """Scattered block tables [B, widest] (unused entries -1) and the pool's block count."""
+    need = [-(-L // bs) for L in lens]
+    total = max(1, sum(need))
+    perm = torch.randperm(total, generator=gen)
+    tab = torch.full((len(lens), max(need + [1])), -1, dtype=torch.int32)
+    at = 0
+    for i, n in enumerate(need):
+        tab[i, :n] = perm[at:at + n].to(torch.int32)
+        at += n
+    return tab, total
+
+
+def _pool(case, blocks, dev_gen):
+    shape = (blocks, case["bs"], case["hkv"], case["d"])
+    if case.get("int8", case["op"] == "varlen"):
+        kv = [torch.randint(-127, 128, shape, generator=dev_gen, device="cuda", dtype=torch.int8) for _ in range(2)]
+        # scales of blocks whose largest entry is 2.5 to 4.5 standard deviations
+        sc = [(torch.rand(shape[0], shape[2], generator=dev_gen, device="cuda") * 2 + 2.5) / 127 for _ in range(2)]
+        return kv + sc
+    return [torch.randn(shape, generator=dev_gen, device="cuda", dtype=DT[case["dtype"]]) for _ in range(2)]
+
+
+def _history(lens, hkv, keys, dev_gen):
+    """Accumulated weights as some hundred steps leave them: few heavy keys, many light ones, the newest at zero."""
+    w = torch.randn(len(lens), hkv, keys, generator=dev_gen, device="cuda").mul_(1.5).exp_()
+    for i, L in enumerate(lens):
+        w[i, :, :L] *= 200.0 / max(1, L)
+        w[i, :, max(0, L - 3):] = 0
+    return w
+
+
+def prepare(case, seed):
+    gen = torch.Generator().manual_seed(seed)
+    dev_gen = torch.Generator(device="cuda").manual_seed(seed + 1)
+    st = {"case": case}
+    if case["op"] == "varlen":
+        q_lens, lens = _rows(case)
+        cu = [0]
+        for n in q_lens:
+            cu.append(cu[-1] + n)
+        st.update(q_lens=q_lens, cu=torch.tensor(cu, dtype=torch.int32, device="cuda"),
+                  q=torch.randn(cu[-1], case["hq"], case["d"], generator=dev_gen, device="cuda", dtype=DT[case["dtype"]]))
+    else:
+        lens = _lengths(case)
+    st["lens"] = lens
+    st["seq_lens"] = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    tab, blocks = _tables(lens, case["bs"], gen)
+    keys = tab.shape[1] * case["bs"]
+    if case["op"] != "select":
+        st["tables"] = tab.cuda()
+        st["pool"] = _pool(case, blocks, dev_gen)
+    if case["op"] in ("decode", "select", "compact"):
+        st["weights"] = _history(lens, case["hkv"], keys, dev_gen)
+    if case["op"] == "decode":
+        st["q"] = torch.randn(len(lens), case["hq"], case["d"], generator=dev_gen, device="cuda", dtype=DT[case["dtype"]])
+    if case["op"] == "compact":
+        st["kept"] = _choose(st["weights"], lens, case["budget"], case["sink"], case["recent"])[0]
+    if own:
+        import pagedattention_decode_gb300 as P
+        st["lib"] = P
+        if case["op"] == "decode":
+            n = P.decode_workspace_size(len(lens), case["hq"], case["hkv"], case["d"], max_keys=keys)
+            st["ws"] = torch.empty(n, dtype=torch.uint8, device="cuda")
+        if case["op"] == "varlen":
+            n = P.varlen_workspace_size(len(lens), case["hq"], case["hkv"], case["d"])
+            st["ws"] = torch.empty(n, dtype=torch.uint8, device="cuda")
+    return st
+
+
+# ---- plain forms -----------------------------------------------------------------
+
+def _gather(st, i, lo, hi):
+    """K and V rows lo..hi-1 of sequence i in 32 bits, [heads, keys, d]."""
+    c, bs = st["case"], st["case"]["bs"]
+    t = torch.arange(lo, hi, device="cuda")
+    blk = st["tables"][i, t // bs].long()
+    off = t % bs
+    p = st["pool"]
+    k, v = p[0][blk, off].float(), p[1][blk, off].float()
+    if len(p) == 4:
+        k, v = k * p[2][blk][:, :, None], v * p[3][blk][:, :, None]
+    return k.transpose(0, 1), v.transpose(0, 1)
+
+
+def _decode_plain(st):
+    c = st["case"]
+    hkv, g, d = c["hkv"], c["hq"] // c["hkv"], c["d"]
+    out = torch.zeros(len(st["lens"]), c["hq"], d, device="cuda")
+    w = st["weights"]
+    for i, L in enumerate(st["lens"]):
+        lo = max(0, L - c["window"]) if c["window"] else 0
+        k, v = _gather(st, i, lo, L)
+        s = torch.matmul(st["q"][i].float().view(hkv, g, d), k.transpose(1, 2)) * d ** -0.5
+        e = torch.exp(s - s.amax(-1, keepdim=True))
+        p = e / e.sum(-1, keepdim=True)
+        out[i] = torch.matmul(p, v).reshape(c["hq"], d)
+        w[i, :, lo:L] += p.sum(1)
+    return out.to(DT[c["dtype"]]), w
+
+
+def _choose(w, lens, budget, sink, recent):
+    """Kept positions [B, H, budget] (-1 past the last) and the new lengths."""
+    B, H, K = w.shape
+    L = torch.tensor(lens, device=w.device)[:, None, None]
+    t = torch.arange(K, device=w.device)[None, None, :]
+    big = torch.full_like(w, float("inf"))
+    key = torch.where((t < sink) | (t >= L - recent), big, w)
+    key = torch.where(t < L, key, -big)
+    n = min(budget, K)
+    first = torch.sort(key, dim=-1, descending=True, stable=True)[1][..., :n]
+    first = torch.where(torch.arange(n, device=w.device) < torch.clamp(L, max=budget), first, torch.full_like(first, K))
+    first = torch.sort(first, dim=-1)[0]
+    kept = torch.full((B, H, budget), -1, dtype=torch.int32, device=w.device)
+    kept[..., :n] = torch.where(first < K, first, torch.full_like(first, -1)).to(torch.int32)
+    return kept, torch.clamp(L[:, 0, 0], max=budget).to(torch.int32)
+
+
+def _requantise(x, block, nblocks):
+    """x [rows, heads, d] of `nblocks` blocks: codes and scales by the largest entry of each block and head."""
+    top = torch.zeros(nblocks, x.shape[1], device=x.device)
+    top = top.scatter_reduce(0, block[:, None].expand(-1, x.shape[1]), x.abs().amax(-1), "amax")
+    scale = top / 127
+    s = scale[block][:, :, None]
+    return torch.where(s > 0, torch.clamp(torch.round(x / s), -127, 127), torch.zeros_like(x)).to(torch.int8), scale
+
+
+def _compact_plain(st):
+    c, p, w = st["case"], st["pool"], st["weights"]
+    bs, hkv = c["bs"], c["hkv"]
+    heads = torch.arange(hkv, device="cuda")[None, :]
+    for i, L in enumerate(st["lens"]):
+        n = min(L, c["budget"])
+        kept = st["kept"][i, :, :n].long().t()                 # [n, heads]
+        dst = torch.arange(n, device="cuda")
+        tab = st["tables"][i].long()
+        sb, so, db, do = tab[kept // bs], kept % bs, tab[dst // bs][:, None], (dst % bs)[:, None]
+        if c["int8"]:
+            blk = dst // bs
+            nb = -(-n // bs)
+            moved = torch.zeros(nb, hkv, device="cuda")
+            moved = moved.index_add(0, blk, (kept != dst[:, None]).float()) > 0
+            for x, sc in ((p[0], p[2]), (p[1], p[3])):
+                rows = x[sb, so, heads]
+                codes, scale = _requantise(rows.float() * sc[sb, heads][:, :, None], blk, nb)
+                x[db, do, heads] = torch.where(moved[blk][:, :, None], codes, rows)
+                sc[tab[:nb]] = torch.where(moved, scale, sc[tab[:nb]])
+        else:
+            for x in p:
+                x[db, do, heads] = x[sb, so, heads]
+        row = w[i].gather(1, kept.t())
+        w[i, :, :L] = 0
+        w[i, :, :n] = row
+
+
+def _varlen_plain(st):
+    c = st["case"]
+    hkv, g, d = c["hkv"], c["hq"] // c["hkv"], c["d"]
+    out = torch.empty(st["q"].shape, device="cuda")
+    at = 0
+    for i, (n, L) in enumerate(zip(st["q_lens"], st["lens"])):
+        k, v = _gather(st, i, 0, L)
+        q = st["q"][at:at + n].float().view(n, hkv, g, d).permute(1, 2, 0, 3).reshape(hkv, g * n, d)
+        s = (torch.matmul(q, k.transpose(1, 2)) * d ** -0.5).view(hkv, g, n, L)
+        last = torch.arange(L - n, L, device="cuda") if c["causal"] else torch.full((n,), L - 1, device="cuda")
+        t = torch.arange(L, device="cuda")
+        hide = t[None, :] > last[:, None]
+        if c["window"]:
+            hide = hide | (t[None, :] <= last[:, None] - c["window"])
+        s = s.masked_fill(hide, float("-inf"))
+        e = torch.exp(s - s.amax(-1, keepdim=True))
+        p = (e / e.sum(-1, keepdim=True)).view(hkv, g * n, L)
+        out[at:at + n] = torch.matmul(p, v).view(hkv, g, n, d).permute(2, 0, 1, 3).reshape(n, c["hq"], d)
+        at += n
+    return out.to(DT[c["dtype"]])
+
+
+def _values(st):
+    """The caches of a compacted state: 16-bit pools as they are, int8 pools as the values they stand for."""
+    p = st["pool"]
+    if len(p) == 2:
+        return p[0], p[1]
+    return p[0] * p[2][:, None, :, None], p[1] * p[3][:, None, :, None]
+
+
+def run(st):
+    c = st["case"]
+    op = c["op"]
+    if not own:
+        if op == "decode":
+            return _decode_plain(st)
+        if op == "select":
+            return _choose(st["weights"], st["lens"], c["budget"], c["sink"], c["recent"])
+        if op == "compact":
+            _compact_plain(st)
+            return (*_values(st), st["weights"])
+        return _varlen_plain(st)
+    P, p = st["lib"], st.get("pool")
+    if op == "decode":
+        call = P.attn_decode_int8 if c["int8"] else P.attn_decode
+        out = call(st["q"], *p, st["tables"], st["seq_lens"], c["d"] ** -0.5, window=c["window"],
+                   out_dtype=DT[c["dtype"]], workspace=st["ws"], key_weights=st["weights"])
+        return out, st["weights"]
+    if op == "select":
+        return P.evict_select(st["weights"], st["seq_lens"], c["budget"], sink=c["sink"], recent=c["recent"])
+    if op == "compact":
+        call = P.evict_compact_int8 if c["int8"] else P.evict_compact
+        call(*p, st["tables"], st["seq_lens"], st["kept"], key_weights=st["weights"])
+        return (*_values(st), st["weights"])
+    return P.attn_varlen_int8(st["q"], *p, st["tables"], st["cu"], st["seq_lens"], max(st["q_lens"]),
+                              c["d"] ** -0.5, causal=c["causal"], window=c["window"], out_dtype=DT[c["dtype"]],
+                              workspace=st["ws"])
+
+
+# ---- the definitions in 64 bits ----------------------------------------------------
+
+def _key_values64(st, i, h):
+    """All keys and values of sequence i and KV head h in 64 bits: block by block through the table."""
+    p, L = st["pool"], st["lens"][i]
+    ids = st["tables"][i, :-(-L // st["case"]["bs"])].long()
+    k, v = p[0][ids, :, h].double(), p[1][ids, :, h].double()
+    if len(p) == 4:
+        k *= p[2][ids, h].double()[:, None, None]
+        v *= p[3][ids, h].double()[:, None, None]
+    return k.flatten(0, 1)[:L], v.flatten(0, 1)[:L]
+
+
+def exact(case, seed):
+    op = case["op"]
+    st = prepare(case, seed)
+    if op == "select":
+        return _select64(st)
+    if op == "compact":
+        return _compact64(st)
+    scale, g = 1.0 / math.sqrt(case["d"]), case["hq"] // case["hkv"]
+    pairs = work(case)["flops"] / 4 / case["d"]
+    if pairs > 1.5e10:
+        return None
+    q_lens = st.get("q_lens", [1] * len(st["lens"]))
+    out = torch.zeros(st["q"].shape, dtype=torch.float64, device="cuda")
+    total = st["weights"].double() if op == "decode" else None
+    begin = 0
+    for i, (n, L) in enumerate(zip(q_lens, st["lens"])):
+        pos = torch.arange(L, device="cuda")
+        bound = torch.arange(L - n + 1, L + 1, device="cuda") if case.get("causal", True) else torch.full((n,), L, device="cuda")
+        seen = pos < bound[:, None]
+        if case["window"]:
+            seen &= pos >= bound[:, None] - case["window"]
+        for h in range(case["hkv"]):
+            k, v = _key_values64(st, i, h)
+            for j in range(h * g, (h + 1) * g):
+                x = scale * (st["q"][begin:begin + n, j].double() @ k.t())
+                prob = torch.softmax(x.masked_fill(~seen, -math.inf), dim=1)
+                out[begin:begin + n, j] = prob @ v
+                if total is not None:
+                    total[i, h, :L] += prob[0]
+        begin += n
+    return (out, total) if op == "decode" else out
+
+
+def _select64(st):
+    c = st["case"]
+    w = st["weights"].double().cpu().numpy()
+    kept = np.full((len(st["lens"]), c["hkv"], c["budget"]), -1, dtype=np.int32)
+    lens = []
+    for i, L in enumerate(st["lens"]):
+        n = min(L, c["budget"])
+        lens.append(n)
+        for h in range(c["hkv"]):
+            if n == L:
+                kept[i, h, :n] = np.arange(n)
+                continue
+            ends = set(range(c["sink"])) | set(range(L - c["recent"], L))
+            order = [t for t in np.argsort(-w[i, h, :L], kind="stable") if t not in ends]
+            kept[i, h, :n] = sorted(list(ends) + order[:n - len(ends)])
+    return torch.from_numpy(kept).cuda(), torch.tensor(lens, dtype=torch.int32, device="cuda")
+
+
+def _compact64(st):
+    c, bs = st["case"], st["case"]["bs"]
+    if sum(st["lens"]) * c["hkv"] * c["d"] > 4.5e8:
+        return None
+    p = st["pool"]
+    src = list(p[:2])
+    dst = [x.double() for x in _values({"pool": [x.double() for x in p]})]
+    w = st["weights"].double()
+    w0 = w.clone()
+    for i, L in enumerate(st["lens"]):
+        n = min(L, c["budget"])
+        ids = st["tables"][i].long()
+        for h in range(c["hkv"]):
+            kept = st["kept"][i, h, :n].long()
+            w[i, h, :L] = 0
+            w[i, h, :n] = w0[i, h, kept]
+            to = torch.arange(n, device="cuda")
+            for at, (a, b) in enumerate(zip(src, dst)):
+                rows = a[ids[kept // bs], kept % bs, h]
+                if c["int8"]:
+                    # an int8 cache is defined by binary32 decisions (as its writer's): value, scale and quotient each
+                    # rounded once; only what the codes then stand for is taken in 64 bits
+                    s = p[2 + at][ids[kept // bs], h][:, None]
+                    pad = -n % bs
+                    full = torch.cat([rows * s, s.new_zeros(pad, c["d"])]).view(-1, bs * c["d"])
+                    step = full.abs().amax(1, keepdim=True) / 127
+                    near = torch.round(full / step.clamp(min=1e-30)).double() * step.double()
+                    still = (torch.cat([kept == to, torch.ones(pad, dtype=torch.bool, device="cuda")]).view(-1, bs)).all(1)
+                    same = torch.cat([rows.double() * s.double(), s.new_zeros(pad, c["d"]).double()]).view(-1, bs * c["d"])
+                    rows = torch.where(still[:, None], same, near).view(-1, c["d"])[:n]
+                    if pad and not bool(still[-1]):  # codes behind the last kept row stay, under the block's new scale
+                        b[ids[n // bs], n % bs:, h] = a[ids[n // bs], n % bs:, h].double() * step[-1].double()
+                else:
+                    rows = rows.double()
+                b[ids[to // bs], to % bs, h] = rows
+    return (*dst, w)
