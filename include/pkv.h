@@ -91,6 +91,7 @@ typedef int32_t pkv_status;
 #define PKV_DEVERR_PAIR 0x4    /* pkv_copy_blocks: src or dst outside [0, num_blocks) (pair skipped) */
 #define PKV_DEVERR_TIMEOUT 0x8 /* a bounded wait inside a kernel ran out; the kernel returned early */
 #define PKV_DEVERR_LENGTH 0x10 /* a sequence longer than its table, or q_len > kv_len (sequence skipped) */
+#define PKV_DEVERR_KEEP 0x20   /* pkv_evict_compact: kept positions that do not ascend, or outside the sequence (row not moved) */
 
 typedef enum pkv_dtype { PKV_F16 = 0, PKV_BF16 = 1, PKV_F32 = 2 } pkv_dtype;
 
@@ -333,6 +334,95 @@ PKV_API pkv_status pkv_attn_decode_int8(const void *q, int64_t q_token_stride, c
                                         void *workspace, size_t workspace_bytes, int32_t *err_word,
                                         pkv_stream stream);
 
+/* ---- a cache bounded by accumulated attention weight ----------------------- */
+/*
+ * Decode attention that also accumulates what each key received: after the
+ * call, for every sequence s, KV head h and attended key t,
+ *     weights[s][h][t] += sum over the query heads of h of softmax weight(t).
+ * Keys outside the window, and entries at or past seq_lens[s], stay as they
+ * were.  out is that of pkv_attn_decode_window / pkv_attn_decode_int8; other
+ * arguments and errors are theirs.
+ *
+ *   weights  device float32 [num_seqs, num_kv_heads, max_keys], entry (s, h, t)
+ *            at s * weights_seq_stride + h * weights_head_stride + t, with
+ *            max_keys = max_blocks_per_seq * block_size; rows do not overlap.
+ *   workspace >= pkv_attn_decode_weights_workspace_size bytes: the decode
+ *            workspace and 4 bytes per (query head, key of the tables' capacity).
+ *
+ * The sums are binary32; a key's entry is touched by one thread per call, so
+ * results do not depend on the order of execution.
+ */
+PKV_API pkv_status pkv_attn_decode_weights_workspace_size(int32_t num_seqs, int32_t num_q_heads,
+                                                          int32_t num_kv_heads, int32_t head_dim,
+                                                          int64_t max_keys, int32_t device, size_t *bytes);
+PKV_API pkv_status pkv_attn_decode_weights(const void *q, int64_t q_token_stride, const pkv_cache *cache,
+                                           const int32_t *block_tables, int32_t max_blocks_per_seq,
+                                           const int32_t *seq_lens, int32_t num_seqs, int32_t num_q_heads,
+                                           float scale, int32_t window, float *weights,
+                                           int64_t weights_seq_stride, int64_t weights_head_stride, void *out,
+                                           int32_t out_dtype, void *workspace, size_t workspace_bytes,
+                                           int32_t *err_word, pkv_stream stream);
+PKV_API pkv_status pkv_attn_decode_int8_weights(const void *q, int64_t q_token_stride, const pkv_cache_i8 *cache,
+                                                const int32_t *block_tables, int32_t max_blocks_per_seq,
+                                                const int32_t *seq_lens, int32_t num_seqs, int32_t num_q_heads,
+                                                float scale, int32_t window, float *weights,
+                                                int64_t weights_seq_stride, int64_t weights_head_stride, void *out,
+                                                int32_t out_dtype, void *workspace, size_t workspace_bytes,
+                                                int32_t *err_word, pkv_stream stream);
+
+/*
+ * Which keys of each KV head stay when sequences are cut to `budget` keys: a
+ * sequence of L <= budget keeps all; a longer one keeps, in every head, its
+ * first `sink` and last `recent` positions and the budget - sink - recent
+ * others of largest weight (NaN counts as above +inf, -0 as +0; ties go to
+ * the lowest position).
+ *
+ *   weights   device float32 [num_seqs, num_kv_heads, max_keys], strides as above.
+ *   kept      device int32 [num_seqs, num_kv_heads, budget]: ascending positions,
+ *             then -1.
+ *   new_lens  device int32 [num_seqs]: min(L, budget); not the seq_lens array.
+ * A length below 0 or above max_keys sets PKV_DEVERR_LENGTH: kept is all -1 and
+ * new_lens the length as it is.  budget > 0, sink + recent <= budget.
+ */
+PKV_API pkv_status pkv_evict_select(const float *weights, int64_t weights_seq_stride, int64_t weights_head_stride,
+                                    int64_t max_keys, const int32_t *seq_lens, int32_t num_seqs,
+                                    int32_t num_kv_heads, int32_t budget, int32_t sink, int32_t recent,
+                                    int32_t *kept, int32_t *new_lens, int32_t *err_word, pkv_stream stream);
+
+/*
+ * Moves the kept rows to the front, in place: of every sequence with
+ * L = seq_lens[s] > budget, row i < budget of KV head h becomes row
+ * kept[s][h][i], in K, V and, where weights is not NULL, the weights, whose
+ * entries budget .. L - 1 become 0.  seq_lens holds the lengths before the cut.
+ * K and V rows at and past the budget are left as they were.  Heads keep
+ * different tokens under one table, so a row of the pool no longer belongs to
+ * one token; attention over the kept keys is unchanged (keys keep whatever
+ * position their rotation gave them).
+ *
+ * The blocks of a sequence that is cut must be its own: a block that another
+ * sequence or the prefix trie also holds is rewritten under it
+ * (pkv_seq_unshare makes them private first; pkv_seq_truncate gives the
+ * emptied blocks back afterwards).  kept must ascend strictly with
+ * i <= kept[i] < L, as pkv_evict_select writes it; an entry that does not sets
+ * PKV_DEVERR_KEEP and its row is not moved.  A bad block id sets
+ * PKV_DEVERR_BLOCK and the row is not moved.
+ *
+ * int8: a block in which some row of the head moves is re-quantised from its
+ * kept rows as pkv_write_kv_int8 does (value = code * scale, new scale =
+ * max|value| / 127, round half to even, all in binary32); other blocks keep
+ * their codes and scales.  Supported: head_dim 64 or 128 (int8: 128),
+ * block_size a multiple of 16 up to 256.
+ */
+PKV_API pkv_status pkv_evict_compact(const pkv_cache *cache, const int32_t *block_tables, int32_t max_blocks_per_seq,
+                                     const int32_t *seq_lens, int32_t num_seqs, const int32_t *kept, int32_t budget,
+                                     float *weights, int64_t weights_seq_stride, int64_t weights_head_stride,
+                                     int32_t *err_word, pkv_stream stream);
+PKV_API pkv_status pkv_evict_compact_int8(const pkv_cache_i8 *cache, const int32_t *block_tables,
+                                          int32_t max_blocks_per_seq, const int32_t *seq_lens, int32_t num_seqs,
+                                          const int32_t *kept, int32_t budget, float *weights,
+                                          int64_t weights_seq_stride, int64_t weights_head_stride,
+                                          int32_t *err_word, pkv_stream stream);
+
 /* ---- a10: block copy for copy-on-write ----------------------------------- */
 /*
  * [P1] Architecture Overview, copy-on-write: when sequences that share a
@@ -414,6 +504,15 @@ PKV_API pkv_status pkv_seq_free(pkv_allocator *a, int32_t seq_id);
 PKV_API pkv_status pkv_seq_append(pkv_allocator *a, const int32_t *seq_ids, const int32_t *counts,
                                   int32_t n, int64_t *out_slots, int64_t slot_capacity,
                                   int64_t *out_pairs, int32_t pair_capacity, int32_t *num_pairs);
+/* The sequence's length becomes num_tokens (at most its length); blocks past the
+ * last one in use are released in table order. */
+PKV_API pkv_status pkv_seq_truncate(pkv_allocator *a, int32_t seq_id, int64_t num_tokens);
+/* Makes every block of the listed sequences (each listed once) private: a block
+ * with refcount > 1 is replaced by a new one and (old, new) reported, as in
+ * pkv_seq_append's copy-on-write; the last holder keeps the block.  All or
+ * nothing.  Copy the pairs before anything is written. */
+PKV_API pkv_status pkv_seq_unshare(pkv_allocator *a, const int32_t *seq_ids, int32_t n, int64_t *out_pairs,
+                                   int32_t pair_capacity, int32_t *num_pairs);
 PKV_API pkv_status pkv_seq_len(const pkv_allocator *a, int32_t seq_id, int64_t *len);
 PKV_API pkv_status pkv_seq_block_table(const pkv_allocator *a, int32_t seq_id, int32_t *out,
                                        int32_t capacity, int32_t *n);

@@ -10,6 +10,10 @@ Calls (names as in the C ABI, without the ``pkv_`` prefix):
 * :func:`write_kv` -- scatter new K/V rows into their slots;
 * :func:`attn_decode` -- one query row per sequence over its paged keys;
 * :func:`attn_varlen` -- packed prefill chunks and decode rows, causal offset;
+* :func:`attn_decode` and :func:`attn_decode_int8` with ``key_weights`` -- the
+  same, adding to every key's accumulated attention weight;
+* :func:`evict_select`, :func:`evict_compact`, :func:`evict_compact_int8` -- a
+  cache cut to a budget of keys by that weight;
 * :func:`copy_blocks` -- block copies for copy-on-write;
 * :class:`BlockAllocator` -- host allocator producing tables, slots and pairs;
 * :class:`StepGraph` -- a CUDA graph of a step built from these calls.
@@ -29,6 +33,7 @@ __all__ = [
     "write_kv", "attn_decode", "attn_varlen", "copy_blocks", "decode_workspace_size",
     "varlen_workspace_size", "check_copy_pairs", "BlockAllocator", "PkvError", "ExhaustedError",
     "DoubleFreeError", "DEVERR", "library_path", "StepGraph", "write_kv_int8", "attn_decode_int8",
+    "evict_select", "evict_compact", "evict_compact_int8",
 ]
 
 _DT = {torch.float16: PKV_F16, torch.bfloat16: PKV_BF16, torch.float32: PKV_F32}
@@ -91,10 +96,50 @@ def write_kv(k: torch.Tensor, v: torch.Tensor, slot_mapping: torch.Tensor, k_cac
                              ctypes.byref(c), _ptr(err), _stream(stream)))
 
 
+def _on_current_device(**tensors: Optional[torch.Tensor]) -> None:
+    """Every given tensor lies on the current CUDA device (where the call's stream is)."""
+    dev = torch.cuda.current_device()
+    for name, t in tensors.items():
+        if t is not None:
+            _cuda(t, name)
+            if t.device.index != dev:
+                raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
+
+
+def _check_err(err: Optional[torch.Tensor]) -> None:
+    if err is not None and (err.dtype != torch.int32 or err.numel() < 1):
+        raise TypeError("err must be an int32 CUDA tensor")
+
+
+def _key_weights(w: torch.Tensor, num_seqs: int, num_kv_heads: int, keys: int, name: str = "key_weights"):
+    """The strides of accumulated weights [B, Hkv, >= keys] float32, keys contiguous."""
+    if w.dtype != torch.float32 or w.dim() != 3:
+        raise TypeError(f"{name} must be float32 [num_seqs, num_kv_heads, max_keys]")
+    if w.shape[0] != num_seqs or w.shape[1] != num_kv_heads or w.shape[2] < keys:
+        raise ValueError(f"{name} must be [{num_seqs}, {num_kv_heads}, {keys} or more] for these tables, "
+                         f"got {list(w.shape)}")
+    if w.shape[2] > 1 and w.stride(2) != 1:
+        raise ValueError(f"{name}: the keys of a head must be contiguous")
+    # strides of dimensions of length 1 are never used: any value that does not overlap
+    head = w.stride(1) if num_kv_heads > 1 else w.shape[2]
+    seq = w.stride(0) if num_seqs > 1 else max(0, num_kv_heads - 1) * head + w.shape[2]
+    return seq, head
+
+
+def _same_rows(num_seqs: int, block_tables: torch.Tensor, seq_lens: torch.Tensor) -> None:
+    if block_tables.dim() != 2 or block_tables.shape[0] != num_seqs or seq_lens.numel() != num_seqs:
+        raise ValueError(f"block_tables must be [{num_seqs}, max_blocks] and seq_lens [{num_seqs}]")
+
+
 def decode_workspace_size(num_seqs: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
-                          device: Optional[int] = None) -> int:
+                          device: Optional[int] = None, max_keys: Optional[int] = None) -> int:
+    """Bytes of a decode call's workspace; with key weights, max_keys = table columns * block_size."""
     n = ctypes.c_size_t(0)
     dev = torch.cuda.current_device() if device is None else device
+    if max_keys is not None:
+        check(lib().pkv_attn_decode_weights_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, max_keys,
+                                                           dev, ctypes.byref(n)))
+        return n.value
     check(lib().pkv_attn_decode_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, dev,
                                                ctypes.byref(n)))
     return n.value
@@ -120,13 +165,17 @@ def attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, b
                 seq_lens: torch.Tensor, scale: float, out: Optional[torch.Tensor] = None,
                 out_dtype: torch.dtype = torch.float32, workspace: Optional[torch.Tensor] = None,
                 err: Optional[torch.Tensor] = None, stream=None, window: int = 0,
-                k_new: Optional[torch.Tensor] = None, v_new: Optional[torch.Tensor] = None) -> torch.Tensor:
+                k_new: Optional[torch.Tensor] = None, v_new: Optional[torch.Tensor] = None,
+                key_weights: Optional[torch.Tensor] = None) -> torch.Tensor:
     """q [B, Hq, D]; tables [B, max_blocks] int32; seq_lens [B] int32 -> out [B, Hq, D].
 
     window > 0 attends only each sequence's most recent ``window`` keys.
     With k_new / v_new [B, Hkv, D], row s is first written to the slot of
     position seq_lens[s] - 1 (from the block table) in the same kernel
-    (pkv_attn_decode_append)."""
+    (pkv_attn_decode_append).  With key_weights (float32 [B, Hkv, >= table
+    columns * block_size]) every attended key's softmax weight, summed over the
+    query heads of its KV head, is added to key_weights[s, h, t]
+    (pkv_attn_decode_weights); not together with k_new / v_new."""
     c = _cache(k_cache, v_cache)
     _cuda(q, "q")
     _check_i32(block_tables, "block_tables")
@@ -138,6 +187,13 @@ def attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, b
         out = torch.empty((B, hq, d), dtype=out_dtype, device=q.device)
     elif not out.is_contiguous() or out.shape != q.shape:
         raise ValueError("out must be contiguous [B, Hq, D]")
+    if key_weights is not None:
+        if k_new is not None or v_new is not None:
+            raise ValueError("key_weights and k_new / v_new do not go together: write the rows first (write_kv)")
+        if hq % c.num_kv_heads or d != c.head_dim:
+            raise ValueError("q must be [B, Hq, D] with Hq a multiple of the cache's heads and its D")
+        return _decode_weights("pkv_attn_decode_weights", c, q, block_tables, seq_lens, scale, window, key_weights, out,
+                               workspace, err, stream)
     ws = _workspace(lambda: decode_workspace_size(B, hq, c.num_kv_heads, d, q.device.index), workspace, q.device)
     mb = block_tables.shape[1] if block_tables.dim() == 2 else 0
     if (k_new is None) != (v_new is None):
@@ -162,6 +218,26 @@ def attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, b
         check(lib().pkv_attn_decode(_ptr(q), _row_stride(q, "q"), ctypes.byref(c), _ptr(block_tables), mb,
                                     _ptr(seq_lens), B, hq, float(scale), _ptr(out), _DT[out.dtype], _ptr(ws),
                                     ws.numel() * ws.element_size(), _ptr(err), _stream(stream)))
+    return out
+
+
+def _decode_weights(call: str, c, q, block_tables, seq_lens, scale, window, key_weights, out, workspace, err, stream):
+    """The decode calls that accumulate key weights (16-bit and int8 caches); out is allocated."""
+    B, hq, d = q.shape
+    _on_current_device(q=q, block_tables=block_tables, seq_lens=seq_lens, key_weights=key_weights, out=out,
+                       workspace=workspace, err=err)
+    _check_err(err)
+    _same_rows(B, block_tables, seq_lens)
+    if out.dtype not in _DT or not out.is_contiguous() or out.shape != q.shape:
+        raise ValueError("out must be contiguous [B, Hq, D] of float32 or q's type")
+    keys = block_tables.shape[1] * c.block_size
+    seq_stride, head_stride = _key_weights(key_weights, B, c.num_kv_heads, keys)
+    ws = _workspace(lambda: decode_workspace_size(B, hq, c.num_kv_heads, d, q.device.index, max_keys=keys), workspace,
+                    q.device)
+    check(getattr(lib(), call)(_ptr(q), _row_stride(q, "q"), ctypes.byref(c), _ptr(block_tables), block_tables.shape[1],
+                               _ptr(seq_lens), B, hq, float(scale), int(window), _ptr(key_weights), seq_stride,
+                               head_stride, _ptr(out), _DT[out.dtype], _ptr(ws), ws.numel() * ws.element_size(),
+                               _ptr(err), _stream(stream)))
     return out
 
 
@@ -237,8 +313,10 @@ def attn_decode_int8(q: torch.Tensor, kq: torch.Tensor, vq: torch.Tensor, k_scal
                      v_scale: torch.Tensor, block_tables: torch.Tensor, seq_lens: torch.Tensor, scale: float,
                      window: int = 0, out: Optional[torch.Tensor] = None, out_dtype: torch.dtype = torch.float32,
                      workspace: Optional[torch.Tensor] = None, err: Optional[torch.Tensor] = None,
-                     stream=None) -> torch.Tensor:
-    """Decode attention over an int8 cache; q fp16/bf16 [B, Hq, D]."""
+                     stream=None, key_weights: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Decode attention over an int8 cache; q fp16/bf16 [B, Hq, D].
+
+    With key_weights, as in :func:`attn_decode` (pkv_attn_decode_int8_weights)."""
     c = _cache_i8(kq, vq, k_scale, v_scale, q.dtype)
     _cuda(q, "q")
     _check_i32(block_tables, "block_tables")
@@ -246,12 +324,91 @@ def attn_decode_int8(q: torch.Tensor, kq: torch.Tensor, vq: torch.Tensor, k_scal
     B, hq, d = q.shape
     if out is None:
         out = torch.empty((B, hq, d), dtype=out_dtype, device=q.device)
+    if key_weights is not None:
+        if hq % c.num_kv_heads or d != c.head_dim:
+            raise ValueError("q must be [B, Hq, D] with Hq a multiple of the cache's heads and its D")
+        return _decode_weights("pkv_attn_decode_int8_weights", c, q, block_tables, seq_lens, scale, window, key_weights,
+                               out, workspace, err, stream)
     ws = _workspace(lambda: decode_workspace_size(B, hq, c.num_kv_heads, d, q.device.index), workspace, q.device)
     check(lib().pkv_attn_decode_int8(_ptr(q), _row_stride(q, "q"), ctypes.byref(c), _ptr(block_tables),
                                      block_tables.shape[1], _ptr(seq_lens), B, hq, float(scale), int(window),
                                      _ptr(out), _DT[out.dtype], _ptr(ws), ws.numel() * ws.element_size(), _ptr(err),
                                      _stream(stream)))
     return out
+
+
+def evict_select(key_weights: torch.Tensor, seq_lens: torch.Tensor, budget: int, sink: int = 0, recent: int = 0,
+                 kept: Optional[torch.Tensor] = None, new_lens: Optional[torch.Tensor] = None,
+                 err: Optional[torch.Tensor] = None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Which positions of every KV head stay when sequences are cut to ``budget`` keys.
+
+    key_weights float32 [B, Hkv, max_keys] (see :func:`attn_decode`), seq_lens [B]
+    int32.  A longer sequence keeps its first ``sink`` and last ``recent``
+    positions and, in each head, those of largest weight besides (ties: the
+    lowest position).  Returns kept [B, Hkv, budget] int32 (ascending, then -1)
+    and new_lens [B] int32 (min(length, budget))."""
+    _on_current_device(key_weights=key_weights, seq_lens=seq_lens, kept=kept, new_lens=new_lens, err=err)
+    _check_err(err)
+    _check_i32(seq_lens, "seq_lens")
+    budget, sink, recent = int(budget), int(sink), int(recent)
+    if budget < 1 or sink < 0 or recent < 0 or sink + recent > budget:
+        raise ValueError(f"budget {budget} must be positive and cover sink {sink} + recent {recent}")
+    if key_weights.dim() != 3:
+        raise TypeError("key_weights must be float32 [num_seqs, num_kv_heads, max_keys]")
+    B, hkv, keys = key_weights.shape
+    if hkv < 1 or seq_lens.numel() != B:
+        raise ValueError(f"seq_lens must have {B} entries and key_weights one KV head or more")
+    seq_stride, head_stride = _key_weights(key_weights, B, hkv, keys)
+    if kept is None:
+        kept = torch.empty((B, hkv, budget), dtype=torch.int32, device=key_weights.device)
+    if new_lens is None:
+        new_lens = torch.empty(B, dtype=torch.int32, device=key_weights.device)
+    _check_i32(kept, "kept")
+    _check_i32(new_lens, "new_lens")
+    if kept.shape != (B, hkv, budget) or new_lens.numel() != B:
+        raise ValueError(f"kept must be [{B}, {hkv}, {budget}] and new_lens [{B}]")
+    check(lib().pkv_evict_select(_ptr(key_weights), seq_stride, head_stride, keys, _ptr(seq_lens), B, hkv, budget, sink,
+                                 recent, _ptr(kept), _ptr(new_lens), _ptr(err), _stream(stream)))
+    return kept, new_lens
+
+
+def _compact(call: str, c, block_tables, seq_lens, kept, key_weights, err, stream, **pools) -> None:
+    _on_current_device(block_tables=block_tables, seq_lens=seq_lens, kept=kept, key_weights=key_weights, err=err, **pools)
+    _check_err(err)
+    for t, n in ((block_tables, "block_tables"), (seq_lens, "seq_lens"), (kept, "kept")):
+        _check_i32(t, n)
+    B = seq_lens.numel()
+    _same_rows(B, block_tables, seq_lens)
+    if kept.dim() != 3 or kept.shape[:2] != (B, c.num_kv_heads) or kept.shape[2] < 1:
+        raise ValueError(f"kept must be [{B}, {c.num_kv_heads}, budget]")
+    seq_stride = head_stride = 0
+    if key_weights is not None:
+        seq_stride, head_stride = _key_weights(key_weights, B, c.num_kv_heads, block_tables.shape[1] * c.block_size)
+    check(getattr(lib(), call)(ctypes.byref(c), _ptr(block_tables), block_tables.shape[1], _ptr(seq_lens), B, _ptr(kept),
+                               kept.shape[2], _ptr(key_weights), seq_stride, head_stride, _ptr(err), _stream(stream)))
+
+
+def evict_compact(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Tensor, seq_lens: torch.Tensor,
+                  kept: torch.Tensor, key_weights: Optional[torch.Tensor] = None, err: Optional[torch.Tensor] = None,
+                  stream=None) -> None:
+    """Moves the kept rows of every sequence longer than the budget to its front, in place.
+
+    kept [B, Hkv, budget] as :func:`evict_select` gives it, seq_lens the lengths
+    before the cut.  With key_weights, a key's weight moves with it and the
+    entries behind the budget become 0.  The sequences' blocks must be their
+    own (:meth:`BlockAllocator.unshare`); afterwards the lengths are
+    min(length, budget) (:meth:`BlockAllocator.truncate`)."""
+    _compact("pkv_evict_compact", _cache(k_cache, v_cache), block_tables, seq_lens, kept, key_weights, err, stream,
+             k_cache=k_cache, v_cache=v_cache)
+
+
+def evict_compact_int8(kq: torch.Tensor, vq: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor,
+                       block_tables: torch.Tensor, seq_lens: torch.Tensor, kept: torch.Tensor,
+                       key_weights: Optional[torch.Tensor] = None, err: Optional[torch.Tensor] = None,
+                       stream=None) -> None:
+    """:func:`evict_compact` over an int8 cache: blocks in which rows of a head move are re-quantised."""
+    _compact("pkv_evict_compact_int8", _cache_i8(kq, vq, k_scale, v_scale, torch.float16), block_tables, seq_lens, kept,
+             key_weights, err, stream, kq=kq, vq=vq, k_scale=k_scale, v_scale=v_scale)
 
 
 def copy_blocks(k_caches: Sequence[torch.Tensor], v_caches: Sequence[torch.Tensor], src_dst_pairs: torch.Tensor,
@@ -373,6 +530,20 @@ class BlockAllocator:
                                    ctypes.c_void_p(pairs_out.data_ptr()), pairs_out.numel() // 2,
                                    ctypes.byref(np_)))
         return np_.value
+
+    def truncate(self, seq_id: int, num_tokens: int) -> None:
+        """The sequence's length becomes num_tokens; blocks past its last one are released."""
+        check(lib().pkv_seq_truncate(self._h, seq_id, num_tokens))
+
+    def unshare(self, seq_ids: Sequence[int]) -> List[Tuple[int, int]]:
+        """Gives the sequences blocks of their own; returns the (old, new) pairs to copy."""
+        n = len(seq_ids)
+        ids = (ctypes.c_int32 * max(1, n))(*seq_ids)
+        cap = sum(len(self.block_table(s)) for s in seq_ids)
+        pairs = (ctypes.c_int64 * max(2, 2 * cap))()
+        np_ = ctypes.c_int32()
+        check(lib().pkv_seq_unshare(self._h, ids, n, pairs, cap, ctypes.byref(np_)))
+        return [(pairs[2 * i], pairs[2 * i + 1]) for i in range(np_.value)]
 
     def seq_len(self, seq_id: int) -> int:
         n = ctypes.c_int64()

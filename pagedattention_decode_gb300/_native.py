@@ -20,7 +20,7 @@ STATUS = {
 }
 PKV_F16, PKV_BF16, PKV_F32 = 0, 1, 2
 PKV_NOALLOC_SCRATCH_BYTES = 16 * 1024 * 1024  # the fixed scratch of pkv_attn_decode_noalloc (pkv.h)
-DEVERR = {"slot": 0x1, "block": 0x2, "pair": 0x4, "timeout": 0x8, "length": 0x10}
+DEVERR = {"slot": 0x1, "block": 0x2, "pair": 0x4, "timeout": 0x8, "length": 0x10, "keep": 0x20}
 
 
 class PkvError(RuntimeError):
@@ -79,6 +79,14 @@ SIGNATURES = {
     "pkv_write_kv_int8": (_i32, [_vp, _vp, _i64, _vp, _i32, _P(PkvCacheI8), _vp, _vp]),
     "pkv_attn_decode_int8": (_i32, [_vp, _i64, _P(PkvCacheI8), _vp, _i32, _vp, _i32, _i32, _f32, _i32, _vp, _i32,
                                     _vp, _sz, _vp, _vp]),
+    "pkv_attn_decode_weights_workspace_size": (_i32, [_i32, _i32, _i32, _i32, _i64, _i32, _P(_sz)]),
+    "pkv_attn_decode_weights": (_i32, [_vp, _i64, _P(PkvCache), _vp, _i32, _vp, _i32, _i32, _f32, _i32, _vp, _i64,
+                                       _i64, _vp, _i32, _vp, _sz, _vp, _vp]),
+    "pkv_attn_decode_int8_weights": (_i32, [_vp, _i64, _P(PkvCacheI8), _vp, _i32, _vp, _i32, _i32, _f32, _i32, _vp,
+                                            _i64, _i64, _vp, _i32, _vp, _sz, _vp, _vp]),
+    "pkv_evict_select": (_i32, [_vp, _i64, _i64, _i64, _vp, _i32, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _vp]),
+    "pkv_evict_compact": (_i32, [_P(PkvCache), _vp, _i32, _vp, _i32, _vp, _i32, _vp, _i64, _i64, _vp, _vp]),
+    "pkv_evict_compact_int8": (_i32, [_P(PkvCacheI8), _vp, _i32, _vp, _i32, _vp, _i32, _vp, _i64, _i64, _vp, _vp]),
     "pkv_copy_blocks": (_i32, [_P(PkvCache), _i32, _vp, _i32, _vp, _vp]),
     "pkv_check_copy_pairs": (_i32, [_vp, _i32, _i32]),
     "pkv_alloc_create": (_i32, [_i32, _i32, _P(_vp)]),
@@ -97,6 +105,8 @@ SIGNATURES = {
     "pkv_seq_fork": (_i32, [_vp, _i32, _P(_i32)]),
     "pkv_seq_free": (_i32, [_vp, _i32]),
     "pkv_seq_append": (_i32, [_vp, _vp, _vp, _i32, _vp, _i64, _vp, _i32, _P(_i32)]),
+    "pkv_seq_truncate": (_i32, [_vp, _i32, _i64]),
+    "pkv_seq_unshare": (_i32, [_vp, _vp, _i32, _vp, _i32, _P(_i32)]),
     "pkv_seq_len": (_i32, [_vp, _i32, _P(_i64)]),
     "pkv_seq_block_table": (_i32, [_vp, _i32, _vp, _i32, _P(_i32)]),
     "pkv_seq_fill_tables": (_i32, [_vp, _vp, _i32, _vp, _i32, _vp]),

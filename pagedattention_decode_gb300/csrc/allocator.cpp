@@ -18,6 +18,7 @@
 #include <algorithm>
 #include <map>
 #include <mutex>
+#include <new>
 #include <unordered_map>
 #include <vector>
 
@@ -306,6 +307,63 @@ pkv_status pkv_seq_append(pkv_allocator *a, const int32_t *seq_ids, const int32_
     }
     *num_pairs = np;
     return pkv::ok();
+}
+
+pkv_status pkv_seq_truncate(pkv_allocator *a, int32_t seq_id, int64_t num_tokens) {
+    PKV_CHECK_ARG(a, PKV_ERR_INVALID_ARG, "NULL allocator");
+    Guard g(a->mu);
+    PKV_CHECK_ARG(a->live_seq(seq_id), PKV_ERR_OUT_OF_RANGE, "sequence %d is not live", seq_id);
+    auto &s = a->seqs[seq_id];
+    PKV_CHECK_ARG(num_tokens >= 0 && num_tokens <= s.len, PKV_ERR_INVALID_ARG,
+                  "sequence %d holds %lld tokens, cannot be cut to %lld", seq_id, (long long)s.len,
+                  (long long)num_tokens);
+    const size_t keep = (size_t)((num_tokens + a->block_size - 1) / a->block_size);
+    for (size_t i = keep; i < s.table.size(); ++i) a->release_one(s.table[i]);
+    s.table.erase(s.table.begin() + std::min(keep, s.table.size()), s.table.end());
+    s.len = num_tokens;
+    return pkv::ok();
+}
+
+pkv_status pkv_seq_unshare(pkv_allocator *a, const int32_t *seq_ids, int32_t n, int64_t *out_pairs,
+                           int32_t pair_capacity, int32_t *num_pairs) {
+    PKV_CHECK_ARG(a && num_pairs && n >= 0 && (seq_ids || n == 0), PKV_ERR_INVALID_ARG, "bad argument");
+    Guard g(a->mu);
+    try {
+        // a block's holders are counted before anything moves: its refcount says how
+        // many of the listed sequences have to leave it
+        std::map<int32_t, int32_t> left;
+        std::map<int32_t, int32_t> seen;
+        int64_t need = 0;
+        for (int32_t i = 0; i < n; ++i) {
+            PKV_CHECK_ARG(a->live_seq(seq_ids[i]), PKV_ERR_OUT_OF_RANGE, "sequence %d is not live", seq_ids[i]);
+            PKV_CHECK_ARG(seen[seq_ids[i]]++ == 0, PKV_ERR_INVALID_ARG, "sequence %d appears twice", seq_ids[i]);
+            for (int32_t id : a->seqs[seq_ids[i]].table)
+                if (a->refcount[id] - left[id] > 1) {
+                    left[id] += 1;
+                    ++need;
+                }
+        }
+        PKV_CHECK_ARG(need <= pair_capacity && (out_pairs || need == 0), PKV_ERR_INVALID_ARG, "pair capacity %d < %lld",
+                      pair_capacity, (long long)need);
+        PKV_CHECK_ARG(need <= (int64_t)a->free_stack.size(), PKV_ERR_EXHAUSTED, "need %lld blocks, %zu free",
+                      (long long)need, a->free_stack.size());
+        int32_t np = 0;
+        for (int32_t i = 0; i < n; ++i)
+            for (int32_t &id : a->seqs[seq_ids[i]].table)
+                if (a->refcount[id] > 1) {
+                    const int32_t dst = a->pop();
+                    out_pairs[2 * np] = id;
+                    out_pairs[2 * np + 1] = dst;
+                    ++np;
+                    a->counters.cow_copies += 1;
+                    a->release_one(id);
+                    id = dst;
+                }
+        *num_pairs = np;
+        return pkv::ok();
+    } catch (const std::bad_alloc &) {  // the bookkeeping above, before anything moved
+        return pkv::fail(PKV_ERR_EXHAUSTED, "out of host memory");
+    }
 }
 
 pkv_status pkv_seq_len(const pkv_allocator *a, int32_t seq_id, int64_t *len) {

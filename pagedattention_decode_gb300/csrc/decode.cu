@@ -116,6 +116,11 @@ struct DecodeParams {
     const void *k_new, *v_new;
     int64_t new_stride;            // elements between consecutive new rows
     void *k_pool, *v_pool;         // the pools ([num_blocks * block_size, hkv, D])
+    // key weights (pkv_attn_decode_weights); NULL otherwise
+    float *key_w;                  // accumulated weights, key (s, h, t) at s * w_seq + h * w_head + t
+    int64_t w_seq, w_head;
+    float *scores;                 // workspace [num_seqs][hkv][max_blocks * block_size][group], in base 2
+    float2 *norm;                  // workspace [num_seqs][hq]: (max, 1 / sum) of a row's softmax
 };
 
 // First key a decode row of a sequence with L keys attends (sliding window).
@@ -221,9 +226,11 @@ __device__ __forceinline__ int range_owner(int64_t x, int64_t total, int64_t cta
 // pass the running max before the max is moved
 constexpr float kLazyMax = 8.f;
 
-// AP: append mode (pkv_attn_decode_append), compiled separately so that the
-// plain decode carries none of its code
-template <int D, typename T, bool I8, bool AP = false>
+// AP: append mode (pkv_attn_decode_append), W: key weights
+// (pkv_attn_decode_weights), each compiled separately so that the plain
+// decode carries none of their code.  W leaves every score and, per finished
+// row, the softmax's max and sum in the workspace for key_weights_kernel.
+template <int D, typename T, bool I8, bool AP = false, bool W = false>
 __global__ void __launch_bounds__(cta_threads<D, I8>(), I8 ? kI8CtasPerSm : (D == 64 ? kD64CtasPerSm : 1))
     decode_splitk_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                          const DecodeParams p) {
@@ -548,7 +555,8 @@ __global__ void __launch_bounds__(cta_threads<D, I8>(), I8 ? kI8CtasPerSm : (D =
         }
         float mA = -INFINITY, mB = -INFINITY, lA = 0.f, lB = 0.f;
         // int8 K codes of an fp16 cache enter the score MMAs as code + 1152 (see i8_pair_biased)
-        constexpr bool BIAS = I8 && IsHalf<T>::value;
+        // (not where the scores themselves leave the kernel: a weight keeps binary32 precision)
+        constexpr bool BIAS = I8 && IsHalf<T>::value && !W;
         float qsA = 0.f, qsB = 0.f;
         if constexpr (BIAS) {
             // sum of q over head_dim for heads hA, hB: lane 4g + t4 holds a quarter of head g
@@ -641,6 +649,19 @@ __global__ void __launch_bounds__(cta_threads<D, I8>(), I8 ? kI8CtasPerSm : (D =
             if (nlo > 0) {
                 if (g < nlo) x0 = x1 = -INFINITY;
                 if (g + 8 < nlo) x2 = x3 = -INFINITY;
+            }
+            if constexpr (W) {
+                // a head's scores of the 16 tokens, masked ones as -inf: the capacity is whole sub-blocks
+                float *sp = p.scores + (((int64_t)s * p.hkv + kvh) * p.max_blocks * p.block_size + tok0) * G;
+                if (G == 1) {
+                    if (t4 == 0) {
+                        sp[g] = x0;
+                        sp[g + 8] = x2;
+                    }
+                } else if (hA < G) {
+                    *reinterpret_cast<float2 *>(sp + g * G + hA) = make_float2(x0, x1);
+                    *reinterpret_cast<float2 *>(sp + (g + 8) * G + hA) = make_float2(x2, x3);
+                }
             }
             if (hA >= gcols) x0 = x2 = 0.f;
             if (hB >= gcols) x1 = x3 = 0.f;
@@ -792,6 +813,13 @@ __global__ void __launch_bounds__(cta_threads<D, I8>(), I8 ? kI8CtasPerSm : (D =
         const bool complete = (sb == 0 && b1 == n_s);
         if (complete) {
             const float iA = 1.f / lA, iB = 1.f / lB;
+            if constexpr (W) {
+                if (g == 0) {
+                    float2 *nm = p.norm + (int64_t)s * p.hkv * G + kvh * G;
+                    if (hA < G) nm[hA] = make_float2(mA, iA);
+                    if (hB < G) nm[hB] = make_float2(mB, iB);
+                }
+            }
             const int64_t ob = (qrow * (int64_t)(p.hkv * G) + (int64_t)kvh * G) * D;
 #pragma unroll
             for (int mt = 0; mt < D / 16; ++mt) {
@@ -875,7 +903,7 @@ constexpr int kMergeThreads = 256;
 // -> 0.2007; A/B, one box).
 constexpr int kMergeScanMaxSeqs = 1024;
 
-template <int D, typename T, int kMergeHeads>
+template <int D, typename T, int kMergeHeads, bool W = false>
 __global__ void __launch_bounds__(kMergeThreads) decode_merge_kernel(const DecodeParams p) {
     extern __shared__ float4 s_merge[];  // [groups][kMergeHeads * D / 4] partial sums, then [parts][heads] weights
     __shared__ int s_scan[32];
@@ -973,6 +1001,9 @@ __global__ void __launch_bounds__(kMergeThreads) decode_merge_kernel(const Decod
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) Lsum += __shfl_xor_sync(0xffffffffu, Lsum, off);
         const float inv = 1.f / Lsum;
+        if constexpr (W) {
+            if (lane == 0) p.norm[(int64_t)s * hq + h] = make_float2(M, inv);
+        }
         for (int c = lane; c < parts; c += 32) s_w[c * kMergeHeads + warp] *= inv;
     }
     __syncthreads();
@@ -1037,7 +1068,71 @@ __global__ void __launch_bounds__(kMergeThreads) decode_merge_kernel(const Decod
     }
 }
 
+// Adds the step's softmax weights to the accumulated ones: a thread takes one
+// key of one (sequence, KV head) and sums its weight over the group's query
+// heads, 2^(score - max) / sum with the row's max and sum, from the scores the
+// decode kernel left.  Reads 4 G + 4 and writes 4 bytes per key beside the
+// decode kernel's 4 G written; with G scores in one vector the accesses are
+// whole lines.
+constexpr int kWeightThreads = 256;
+
+template <int G>
+__global__ void __launch_bounds__(kWeightThreads) key_weights_kernel(const DecodeParams p, int chunks) {
+    pdl_wait();
+    pdl_trigger();
+    const int64_t row = blockIdx.x / chunks;   // (sequence, KV head)
+    const int t = (int)(blockIdx.x % chunks) * kWeightThreads + threadIdx.x;
+    const int64_t s = row / p.hkv;
+    const int h = (int)(row - s * p.hkv);
+    const int L = p.seq_lens[s];
+    const int64_t cap = (int64_t)p.max_blocks * p.block_size;
+    if (L > cap || t >= L || t < decode_first_key(p, L)) return;
+    const float *sp = p.scores + (row * cap + t) * G;
+    float x[G];
+    if constexpr (G == 1) {
+        x[0] = sp[0];
+    } else if constexpr (G == 2) {
+        const float2 a = *reinterpret_cast<const float2 *>(sp);
+        x[0] = a.x;
+        x[1] = a.y;
+    } else {
+#pragma unroll
+        for (int i = 0; i < G; i += 4) {
+            const float4 a = *reinterpret_cast<const float4 *>(sp + i);
+            x[i] = a.x;
+            x[i + 1] = a.y;
+            x[i + 2] = a.z;
+            x[i + 3] = a.w;
+        }
+    }
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < G; ++i) {
+        const float2 nm = p.norm[row * G + i];
+        sum += fast_exp2(x[i] - nm.x) * nm.y;
+    }
+    p.key_w[s * p.w_seq + h * p.w_head + t] += sum;
+}
+
+static pkv_status launch_key_weights(const DecodeParams &p, cudaStream_t stream) {
+    const int64_t cap = (int64_t)p.max_blocks * p.block_size;
+    const int64_t chunks = (cap + kWeightThreads - 1) / kWeightThreads;
+    const int64_t ctas = chunks * p.num_seqs * p.hkv;
+    if (ctas == 0) return PKV_OK;
+    auto kern = p.group == 1   ? key_weights_kernel<1>
+                : p.group == 2 ? key_weights_kernel<2>
+                : p.group == 4 ? key_weights_kernel<4>
+                               : key_weights_kernel<8>;
+    return launch_pdl(kern, dim3((unsigned)ctas), dim3(kWeightThreads), 0, stream, p, (int)chunks);
+}
+
 // ---- host side -------------------------------------------------------------
+
+// The key-weight arguments of a decode call (w == NULL: none).
+struct KeyWeights {
+    float *w = nullptr;
+    int64_t seq_stride = 0, head_stride = 0;
+};
 
 struct DecodePlan {
     int heads_per_cta, num_hg, stages, threads, smem_bytes, cmax;
@@ -1080,10 +1175,10 @@ static pkv_status make_plan(int32_t num_seqs, int32_t num_q_heads, int32_t hkv, 
     return PKV_OK;
 }
 
-template <int D, typename T, bool I8 = false, bool AP = false>
+template <int D, typename T, bool I8 = false, bool AP = false, bool W = false>
 static pkv_status launch_decode_t(const CUtensorMap &mk, const CUtensorMap &mv, const DecodeParams &p,
                                   const DecodePlan &pl, cudaStream_t stream) {
-    auto kern = decode_splitk_kernel<D, T, I8, AP>;
+    auto kern = decode_splitk_kernel<D, T, I8, AP, W>;
     // the plan's shared memory depends only on (D, heads per CTA); size for the largest plan once
     static std::atomic<uint64_t> smem_set{0};
     pkv_status st = set_smem_once(reinterpret_cast<const void *>(kern), 210 * 1024, &smem_set);
@@ -1104,7 +1199,7 @@ static pkv_status launch_decode_t(const CUtensorMap &mk, const CUtensorMap &mv, 
     // a call the small-call split surely covers (total <= bound, grid = a CTA
     // per sequence) cuts no sequence, and its empty rows are written by the
     // decode kernel: no merge
-    if (whole_seq_split(bound, p.num_seqs, grid_x)) return PKV_OK;
+    if (whole_seq_split(bound, p.num_seqs, grid_x)) return W ? launch_key_weights(pg, stream) : PKV_OK;
     // the merge reads only what the decode kernel wrote: launch it as a
     // programmatic dependent so it is scheduled while the decode kernel drains
     // many sequences: 8 query heads per merge CTA (fewer, mostly idle, CTAs);
@@ -1122,9 +1217,25 @@ static pkv_status launch_decode_t(const CUtensorMap &mk, const CUtensorMap &mv, 
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    auto merge = mh == 8 ? decode_merge_kernel<D, T, 8> : mh == 4 ? decode_merge_kernel<D, T, 4> : decode_merge_kernel<D, T, 1>;
+    auto merge = mh == 8   ? decode_merge_kernel<D, T, 8, W>
+                 : mh == 4 ? decode_merge_kernel<D, T, 4, W>
+                           : decode_merge_kernel<D, T, 1, W>;
     PKV_CUDA_TRY(cudaLaunchKernelEx(&cfg, merge, pg));
-    return PKV_OK;
+    return W ? launch_key_weights(pg, stream) : PKV_OK;
+}
+
+// Workspace of the key weights behind the decode plan's: norms, then scores.
+static size_t weights_bytes(int32_t num_seqs, int32_t num_q_heads, int64_t max_keys) {
+    const size_t rows = (size_t)num_seqs * num_q_heads;
+    return round256(rows * sizeof(float2)) + round256(rows * (size_t)max_keys * sizeof(float));
+}
+
+static void set_key_weights(DecodeParams *p, const KeyWeights &kw, uint8_t *ws, int32_t num_q_heads) {
+    p->key_w = kw.w;
+    p->w_seq = kw.seq_stride;
+    p->w_head = kw.head_stride;
+    p->norm = reinterpret_cast<float2 *>(ws);
+    p->scores = reinterpret_cast<float *>(ws + round256((size_t)p->num_seqs * num_q_heads * sizeof(float2)));
 }
 
 // Shared by pkv_attn_decode[_window|_append] (cu_q == NULL) and pkv_attn_varlen[_window] (q_len == 1 rows).
@@ -1132,11 +1243,13 @@ static pkv_status run_decode_impl(const void *q, int64_t q_stride, const pkv_cac
                                   int32_t max_blocks, const int32_t *seq_lens, const int32_t *cu_q, int32_t num_seqs,
                                   int32_t num_q_heads, float scale, int32_t window, void *out, int32_t out_dtype,
                                   void *workspace, size_t workspace_bytes, int32_t *err_word, cudaStream_t stream,
-                                  const void *k_new, const void *v_new, int64_t new_stride) {
+                                  const void *k_new, const void *v_new, int64_t new_stride,
+                                  const KeyWeights &kw = KeyWeights()) {
     DecodePlan pl;
     pkv_status st = make_plan(num_seqs, num_q_heads, cache->num_kv_heads, cache->head_dim, -1, &pl);
     if (st != PKV_OK) return st;
-    const size_t need = pl.meta_bytes + pl.ml_bytes + pl.o_bytes;
+    const size_t base = pl.meta_bytes + pl.ml_bytes + pl.o_bytes;
+    const size_t need = base + (kw.w ? weights_bytes(num_seqs, num_q_heads, (int64_t)max_blocks * cache->block_size) : 0);
     PKV_CHECK_ARG(workspace && workspace_bytes >= need, PKV_ERR_WORKSPACE,
                   "workspace of %zu bytes given, %zu needed", workspace_bytes, need);
     PKV_CHECK_ARG((reinterpret_cast<uintptr_t>(workspace) & 255) == 0, PKV_ERR_INVALID_ARG,
@@ -1177,6 +1290,14 @@ static pkv_status run_decode_impl(const void *q, int64_t q_stride, const pkv_cac
     p.k_pool = cache->k;
     p.v_pool = cache->v;
     const bool bf = cache->dtype == PKV_BF16;
+    if (kw.w) {
+        set_key_weights(&p, kw, ws + base, num_q_heads);
+        if (cache->head_dim == 64)
+            return bf ? launch_decode_t<64, __nv_bfloat16, false, false, true>(mk, mv, p, pl, stream)
+                      : launch_decode_t<64, __half, false, false, true>(mk, mv, p, pl, stream);
+        return bf ? launch_decode_t<128, __nv_bfloat16, false, false, true>(mk, mv, p, pl, stream)
+                  : launch_decode_t<128, __half, false, false, true>(mk, mv, p, pl, stream);
+    }
     if (k_new != nullptr) {
         if (cache->head_dim == 64)
             return bf ? launch_decode_t<64, __nv_bfloat16, false, true>(mk, mv, p, pl, stream)
@@ -1209,14 +1330,16 @@ pkv_status run_decode(const void *q, int64_t q_stride, const pkv_cache *cache, c
 
 pkv_status check_cache_i8(const pkv_cache_i8 *c, const char *what);  // int8_write.cu
 
-static pkv_status run_decode_i8(const void *q, int64_t q_stride, const pkv_cache_i8 *cache, const int32_t *tables,
-                                int32_t max_blocks, const int32_t *seq_lens, int32_t num_seqs, int32_t num_q_heads,
-                                float scale, int32_t window, void *out, int32_t out_dtype, void *workspace,
-                                size_t workspace_bytes, int32_t *err_word, cudaStream_t stream) {
+static pkv_status run_decode_i8_impl(const void *q, int64_t q_stride, const pkv_cache_i8 *cache, const int32_t *tables,
+                                     int32_t max_blocks, const int32_t *seq_lens, const int32_t *cu_q,
+                                     int32_t num_seqs, int32_t num_q_heads, float scale, int32_t window, void *out,
+                                     int32_t out_dtype, void *workspace, size_t workspace_bytes, int32_t *err_word,
+                                     cudaStream_t stream, const KeyWeights &kw = KeyWeights()) {
     DecodePlan pl;
     pkv_status st = make_plan(num_seqs, num_q_heads, cache->num_kv_heads, cache->head_dim, -1, &pl, true);
     if (st != PKV_OK) return st;
-    const size_t need = pl.meta_bytes + pl.ml_bytes + pl.o_bytes;
+    const size_t base = pl.meta_bytes + pl.ml_bytes + pl.o_bytes;
+    const size_t need = base + (kw.w ? weights_bytes(num_seqs, num_q_heads, (int64_t)max_blocks * cache->block_size) : 0);
     PKV_CHECK_ARG(workspace && workspace_bytes >= need, PKV_ERR_WORKSPACE,
                   "workspace of %zu bytes given, %zu needed", workspace_bytes, need);
     PKV_CHECK_ARG((reinterpret_cast<uintptr_t>(workspace) & 255) == 0, PKV_ERR_INVALID_ARG,
@@ -1232,7 +1355,7 @@ static pkv_status run_decode_i8(const void *q, int64_t q_stride, const pkv_cache
     p.tables = tables;
     p.max_blocks = max_blocks;
     p.seq_lens = seq_lens;
-    p.cu_q = nullptr;
+    p.cu_q = cu_q;
     p.num_seqs = num_seqs;
     p.num_blocks = cache->num_blocks;
     p.block_size = cache->block_size;
@@ -1252,8 +1375,22 @@ static pkv_status run_decode_i8(const void *q, int64_t q_stride, const pkv_cache
     p.window = window > 0 ? window : 0;
     p.k_scale = cache->k_scale;
     p.v_scale = cache->v_scale;
+    if (kw.w) {
+        set_key_weights(&p, kw, ws + base, num_q_heads);
+        return cache->dtype == PKV_BF16 ? launch_decode_t<128, __nv_bfloat16, true, false, true>(mk, mv, p, pl, stream)
+                                        : launch_decode_t<128, __half, true, false, true>(mk, mv, p, pl, stream);
+    }
     return cache->dtype == PKV_BF16 ? launch_decode_t<128, __nv_bfloat16, true>(mk, mv, p, pl, stream)
                                     : launch_decode_t<128, __half, true>(mk, mv, p, pl, stream);
+}
+
+// Rows of q_len == 1 of a packed step over an int8 cache (cu_q), or a decode call (cu_q == NULL).
+pkv_status run_decode_i8(const void *q, int64_t q_stride, const pkv_cache_i8 *cache, const int32_t *tables,
+                         int32_t max_blocks, const int32_t *seq_lens, const int32_t *cu_q, int32_t num_seqs,
+                         int32_t num_q_heads, float scale, int32_t window, void *out, int32_t out_dtype,
+                         void *workspace, size_t workspace_bytes, int32_t *err_word, cudaStream_t stream) {
+    return run_decode_i8_impl(q, q_stride, cache, tables, max_blocks, seq_lens, cu_q, num_seqs, num_q_heads, scale,
+                              window, out, out_dtype, workspace, workspace_bytes, err_word, stream);
 }
 
 // Workspace of the 16-bit decode plan (the no-allocation entry point sizes its call with this).
@@ -1267,7 +1404,7 @@ pkv_status decode_workspace_size(int32_t num_seqs, int32_t num_q_heads, int32_t 
 }
 
 // The larger of the 16-bit and int8 plans: one workspace serves every decode call.
-static pkv_status decode_workspace_size_any(int32_t num_seqs, int32_t num_q_heads, int32_t hkv, int32_t head_dim,
+pkv_status decode_workspace_size_any(int32_t num_seqs, int32_t num_q_heads, int32_t hkv, int32_t head_dim,
                                             int32_t device, size_t *bytes) {
     size_t a = 0;
     pkv_status st = decode_workspace_size(num_seqs, num_q_heads, hkv, head_dim, device, &a);
@@ -1297,6 +1434,31 @@ pkv_status check_attention_common(const void *q, int64_t q_stride, const pkv_cac
     if (num_seqs > 0)
         PKV_CHECK_ARG(q && tables && seq_lens && out, PKV_ERR_INVALID_ARG, "%s: NULL pointer", what);
     PKV_CHECK_ARG(aligned16(out), PKV_ERR_INVALID_ARG, "%s: out must be 16-byte aligned", what);
+    return PKV_OK;
+}
+
+pkv_status check_attention_i8(const void *q, int64_t q_token_stride, const pkv_cache_i8 *cache,
+                              const int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *seq_lens,
+                              int32_t num_seqs, int32_t num_q_heads, const void *out, int32_t out_dtype,
+                              const char *what) {
+    pkv_status st = check_cache_i8(cache, what);
+    if (st != PKV_OK) return st;
+    PKV_CHECK_ARG(cache->head_dim == 128, PKV_ERR_UNSUPPORTED, "int8 decode: head_dim must be 128");
+    PKV_CHECK_ARG(cache->num_kv_heads % 4 == 0, PKV_ERR_UNSUPPORTED, "int8 decode: num_kv_heads must be a multiple of 4");
+    PKV_CHECK_ARG(cache->block_size % 16 == 0, PKV_ERR_UNSUPPORTED, "int8 decode: block_size must be a multiple of 16");
+    PKV_CHECK_ARG(num_q_heads > 0 && num_q_heads % cache->num_kv_heads == 0, PKV_ERR_SHAPE,
+                  "num_q_heads must be a multiple of num_kv_heads");
+    const int group = num_q_heads / cache->num_kv_heads;
+    PKV_CHECK_ARG(group == 1 || group == 2 || group == 4 || group == 8, PKV_ERR_UNSUPPORTED,
+                  "query heads per KV head must be 1, 2, 4 or 8");
+    PKV_CHECK_ARG(num_seqs >= 0 && max_blocks_per_seq >= 0, PKV_ERR_INVALID_ARG, "negative size");
+    PKV_CHECK_ARG(out_dtype == PKV_F32 || out_dtype == cache->dtype, PKV_ERR_DTYPE, "out dtype must be F32 or q's");
+    PKV_CHECK_ARG(q_token_stride >= (int64_t)num_q_heads * 128 && q_token_stride % 2 == 0 &&
+                      (reinterpret_cast<uintptr_t>(q) & 7) == 0,
+                  PKV_ERR_INVALID_ARG, "q rows must be 8-byte aligned and at least one row long");
+    PKV_CHECK_ARG(aligned16(out), PKV_ERR_INVALID_ARG, "out must be 16-byte aligned");
+    if (num_seqs == 0) return PKV_OK;
+    PKV_CHECK_ARG(q && block_tables && seq_lens && out, PKV_ERR_INVALID_ARG, "NULL pointer");
     return PKV_OK;
 }
 
@@ -1366,26 +1528,85 @@ pkv_status pkv_attn_decode_int8(const void *q, int64_t q_token_stride, const pkv
                                 int32_t num_seqs, int32_t num_q_heads, float scale, int32_t window, void *out,
                                 int32_t out_dtype, void *workspace, size_t workspace_bytes, int32_t *err_word,
                                 pkv_stream stream) {
-    pkv_status st = check_cache_i8(cache, "pkv_attn_decode_int8");
+    pkv_status st = check_attention_i8(q, q_token_stride, cache, block_tables, max_blocks_per_seq, seq_lens, num_seqs,
+                                       num_q_heads, out, out_dtype, "pkv_attn_decode_int8");
     if (st != PKV_OK) return st;
-    PKV_CHECK_ARG(cache->head_dim == 128, PKV_ERR_UNSUPPORTED, "int8 decode: head_dim must be 128");
-    PKV_CHECK_ARG(cache->num_kv_heads % 4 == 0, PKV_ERR_UNSUPPORTED, "int8 decode: num_kv_heads must be a multiple of 4");
-    PKV_CHECK_ARG(cache->block_size % 16 == 0, PKV_ERR_UNSUPPORTED, "int8 decode: block_size must be a multiple of 16");
-    PKV_CHECK_ARG(num_q_heads > 0 && num_q_heads % cache->num_kv_heads == 0, PKV_ERR_SHAPE,
-                  "num_q_heads must be a multiple of num_kv_heads");
-    const int group = num_q_heads / cache->num_kv_heads;
-    PKV_CHECK_ARG(group == 1 || group == 2 || group == 4 || group == 8, PKV_ERR_UNSUPPORTED,
-                  "query heads per KV head must be 1, 2, 4 or 8");
-    PKV_CHECK_ARG(num_seqs >= 0 && max_blocks_per_seq >= 0, PKV_ERR_INVALID_ARG, "negative size");
-    PKV_CHECK_ARG(out_dtype == PKV_F32 || out_dtype == cache->dtype, PKV_ERR_DTYPE, "out dtype must be F32 or q's");
-    PKV_CHECK_ARG(q_token_stride >= (int64_t)num_q_heads * 128 && q_token_stride % 2 == 0 &&
-                      (reinterpret_cast<uintptr_t>(q) & 7) == 0,
-                  PKV_ERR_INVALID_ARG, "q rows must be 8-byte aligned and at least one row long");
-    PKV_CHECK_ARG(aligned16(out), PKV_ERR_INVALID_ARG, "out must be 16-byte aligned");
     if (num_seqs == 0) return ok();
-    PKV_CHECK_ARG(q && block_tables && seq_lens && out, PKV_ERR_INVALID_ARG, "NULL pointer");
-    st = run_decode_i8(q, q_token_stride, cache, block_tables, max_blocks_per_seq, seq_lens, num_seqs, num_q_heads,
-                       scale, window, out, out_dtype, workspace, workspace_bytes, err_word, stream);
+    st = run_decode_i8(q, q_token_stride, cache, block_tables, max_blocks_per_seq, seq_lens, nullptr, num_seqs,
+                       num_q_heads, scale, window, out, out_dtype, workspace, workspace_bytes, err_word, stream);
+    return st == PKV_OK ? ok() : st;
+}
+
+pkv_status pkv_attn_decode_weights_workspace_size(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
+                                                  int32_t head_dim, int64_t max_keys, int32_t device, size_t *bytes) {
+    PKV_CHECK_ARG(bytes && num_seqs >= 0 && num_kv_heads > 0 && num_q_heads > 0 && head_dim > 0 && max_keys >= 0 &&
+                      max_keys < (int64_t)1 << 31,
+                  PKV_ERR_INVALID_ARG, "bad argument");
+    pkv_status st = decode_workspace_size_any(num_seqs, num_q_heads, num_kv_heads, head_dim, device, bytes);
+    if (st != PKV_OK) return st;
+    *bytes += weights_bytes(num_seqs, num_q_heads, max_keys);
+    return ok();
+}
+
+// The arguments of the accumulated weights, and the range of the launch's grid.
+static pkv_status check_key_weights(const float *weights, int64_t seq_stride, int64_t head_stride, int32_t max_blocks,
+                                    int32_t bs, int32_t hkv, int32_t num_seqs, const char *what) {
+    PKV_CHECK_ARG(weights, PKV_ERR_INVALID_ARG, "%s: weights is NULL", what);
+    PKV_CHECK_ARG((reinterpret_cast<uintptr_t>(weights) & 3) == 0, PKV_ERR_INVALID_ARG,
+                  "%s: weights must be 4-byte aligned", what);
+    const int64_t keys = (int64_t)max_blocks * bs;
+    PKV_CHECK_ARG(keys < (int64_t)1 << 31, PKV_ERR_SHAPE, "%s: tables cover 2^31 keys or more", what);
+    PKV_CHECK_ARG(head_stride >= keys && seq_stride >= (hkv - 1) * head_stride + keys, PKV_ERR_SHAPE,
+                  "%s: weights rows shorter than the tables' %lld keys, or overlapping", what, (long long)keys);
+    PKV_CHECK_ARG((keys + kWeightThreads - 1) / kWeightThreads * num_seqs * hkv < (int64_t)1 << 31, PKV_ERR_UNSUPPORTED,
+                  "%s: num_seqs * num_kv_heads * keys too large", what);
+    return PKV_OK;
+}
+
+pkv_status pkv_attn_decode_weights(const void *q, int64_t q_token_stride, const pkv_cache *cache,
+                                   const int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *seq_lens,
+                                   int32_t num_seqs, int32_t num_q_heads, float scale, int32_t window, float *weights,
+                                   int64_t weights_seq_stride, int64_t weights_head_stride, void *out,
+                                   int32_t out_dtype, void *workspace, size_t workspace_bytes, int32_t *err_word,
+                                   pkv_stream stream) {
+    const char *what = "pkv_attn_decode_weights";
+    pkv_status st = check_attention_common(q, q_token_stride, cache, block_tables, max_blocks_per_seq, seq_lens,
+                                           num_seqs, num_q_heads, out, out_dtype, what);
+    if (st != PKV_OK) return st;
+    if (num_seqs == 0) return ok();
+    st = check_key_weights(weights, weights_seq_stride, weights_head_stride, max_blocks_per_seq, cache->block_size,
+                           cache->num_kv_heads, num_seqs, what);
+    if (st != PKV_OK) return st;
+    KeyWeights kw;
+    kw.w = weights;
+    kw.seq_stride = weights_seq_stride;
+    kw.head_stride = weights_head_stride;
+    st = run_decode_impl(q, q_token_stride, cache, block_tables, max_blocks_per_seq, seq_lens, nullptr, num_seqs,
+                         num_q_heads, scale, window, out, out_dtype, workspace, workspace_bytes, err_word, stream,
+                         nullptr, nullptr, 0, kw);
+    return st == PKV_OK ? ok() : st;
+}
+
+pkv_status pkv_attn_decode_int8_weights(const void *q, int64_t q_token_stride, const pkv_cache_i8 *cache,
+                                        const int32_t *block_tables, int32_t max_blocks_per_seq,
+                                        const int32_t *seq_lens, int32_t num_seqs, int32_t num_q_heads, float scale,
+                                        int32_t window, float *weights, int64_t weights_seq_stride,
+                                        int64_t weights_head_stride, void *out, int32_t out_dtype, void *workspace,
+                                        size_t workspace_bytes, int32_t *err_word, pkv_stream stream) {
+    const char *what = "pkv_attn_decode_int8_weights";
+    pkv_status st = check_attention_i8(q, q_token_stride, cache, block_tables, max_blocks_per_seq, seq_lens, num_seqs,
+                                       num_q_heads, out, out_dtype, what);
+    if (st != PKV_OK) return st;
+    if (num_seqs == 0) return ok();
+    st = check_key_weights(weights, weights_seq_stride, weights_head_stride, max_blocks_per_seq, cache->block_size,
+                           cache->num_kv_heads, num_seqs, what);
+    if (st != PKV_OK) return st;
+    KeyWeights kw;
+    kw.w = weights;
+    kw.seq_stride = weights_seq_stride;
+    kw.head_stride = weights_head_stride;
+    st = run_decode_i8_impl(q, q_token_stride, cache, block_tables, max_blocks_per_seq, seq_lens, nullptr, num_seqs,
+                            num_q_heads, scale, window, out, out_dtype, workspace, workspace_bytes, err_word, stream, kw);
     return st == PKV_OK ? ok() : st;
 }
 
