@@ -334,6 +334,24 @@ PKV_API pkv_status pkv_attn_decode_int8(const void *q, int64_t q_token_stride, c
                                         void *workspace, size_t workspace_bytes, int32_t *err_word,
                                         pkv_stream stream);
 
+/*
+ * Packed prefill chunks and decode rows over an int8 cache: rows, lengths,
+ * masks, workspace size (pkv_attn_varlen_workspace_size) and errors are those
+ * of pkv_attn_varlen_window, cache and arithmetic those of
+ * pkv_attn_decode_int8 (rows of q_len == 1 are that call's).  In a chunk the
+ * codes enter both matrix products exactly; k_scale multiplies the scores in
+ * binary32, and v_scale the softmax weights, which enter P V as a bf16 hi + lo
+ * pair (~16 significant bits) whatever the cache's dtype.  q and its row
+ * stride must be 16-byte aligned when max_q_len > 1, 8-byte otherwise.
+ */
+PKV_API pkv_status pkv_attn_varlen_int8(const void *q, int64_t q_token_stride, const pkv_cache_i8 *cache,
+                                        const int32_t *block_tables, int32_t max_blocks_per_seq,
+                                        const int32_t *cu_seqlens_q, const int32_t *seq_lens,
+                                        int32_t num_seqs, int32_t total_q, int32_t max_q_len,
+                                        int32_t num_q_heads, float scale, int32_t causal, int32_t window,
+                                        void *out, int32_t out_dtype, void *workspace, size_t workspace_bytes,
+                                        int32_t *err_word, pkv_stream stream);
+
 /* ---- a cache bounded by accumulated attention weight ----------------------- */
 /*
  * Decode attention that also accumulates what each key received: after the

@@ -10,6 +10,8 @@ Calls (names as in the C ABI, without the ``pkv_`` prefix):
 * :func:`write_kv` -- scatter new K/V rows into their slots;
 * :func:`attn_decode` -- one query row per sequence over its paged keys;
 * :func:`attn_varlen` -- packed prefill chunks and decode rows, causal offset;
+* :func:`write_kv_int8`, :func:`attn_decode_int8`, :func:`attn_varlen_int8` --
+  the same over an int8 cache;
 * :func:`attn_decode` and :func:`attn_decode_int8` with ``key_weights`` -- the
   same, adding to every key's accumulated attention weight;
 * :func:`evict_select`, :func:`evict_compact`, :func:`evict_compact_int8` -- a
@@ -33,7 +35,7 @@ __all__ = [
     "write_kv", "attn_decode", "attn_varlen", "copy_blocks", "decode_workspace_size",
     "varlen_workspace_size", "check_copy_pairs", "BlockAllocator", "PkvError", "ExhaustedError",
     "DoubleFreeError", "DEVERR", "library_path", "StepGraph", "write_kv_int8", "attn_decode_int8",
-    "evict_select", "evict_compact", "evict_compact_int8",
+    "attn_varlen_int8", "evict_select", "evict_compact", "evict_compact_int8",
 ]
 
 _DT = {torch.float16: PKV_F16, torch.bfloat16: PKV_BF16, torch.float32: PKV_F32}
@@ -234,7 +236,7 @@ def _decode_weights(call: str, c, q, block_tables, seq_lens, scale, window, key_
     seq_stride, head_stride = _key_weights(key_weights, B, c.num_kv_heads, keys)
     ws = _workspace(lambda: decode_workspace_size(B, hq, c.num_kv_heads, d, q.device.index, max_keys=keys), workspace,
                     q.device)
-    check(getattr(lib(), call)(_ptr(q), _row_stride(q, "q"), ctypes.byref(c), _ptr(block_tables), block_tables.shape[1],
+    check(getattr(lib(), call)(_ptr(q), _row_stride(q, "q") if B else hq * d, ctypes.byref(c), _ptr(block_tables), block_tables.shape[1],
                                _ptr(seq_lens), B, hq, float(scale), int(window), _ptr(key_weights), seq_stride,
                                head_stride, _ptr(out), _DT[out.dtype], _ptr(ws), ws.numel() * ws.element_size(),
                                _ptr(err), _stream(stream)))
@@ -334,6 +336,38 @@ def attn_decode_int8(q: torch.Tensor, kq: torch.Tensor, vq: torch.Tensor, k_scal
                                      block_tables.shape[1], _ptr(seq_lens), B, hq, float(scale), int(window),
                                      _ptr(out), _DT[out.dtype], _ptr(ws), ws.numel() * ws.element_size(), _ptr(err),
                                      _stream(stream)))
+    return out
+
+
+def attn_varlen_int8(q: torch.Tensor, kq: torch.Tensor, vq: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor,
+                     block_tables: torch.Tensor, cu_seqlens_q: torch.Tensor, seq_lens: torch.Tensor, max_q_len: int,
+                     scale: float, causal: bool = True, window: int = 0, out: Optional[torch.Tensor] = None,
+                     out_dtype: torch.dtype = torch.float32, workspace: Optional[torch.Tensor] = None,
+                     err: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """:func:`attn_varlen` over an int8 cache: packed rows q fp16/bf16 [total_q, Hq, D],
+    cu_seqlens_q [B+1], seq_lens = kv_len [B], the new rows' keys already written."""
+    c = _cache_i8(kq, vq, k_scale, v_scale, q.dtype)
+    _on_current_device(q=q, kq=kq, vq=vq, k_scale=k_scale, v_scale=v_scale, block_tables=block_tables,
+                       cu_seqlens_q=cu_seqlens_q, seq_lens=seq_lens, out=out, workspace=workspace, err=err)
+    _check_err(err)
+    for t, n in ((block_tables, "block_tables"), (seq_lens, "seq_lens"), (cu_seqlens_q, "cu_seqlens_q")):
+        _check_i32(t, n)
+    B = seq_lens.numel()
+    _same_rows(B, block_tables, seq_lens)
+    if cu_seqlens_q.numel() != B + 1:
+        raise ValueError("cu_seqlens_q must have num_seqs + 1 entries")
+    if q.dim() != 3 or q.shape[1] % c.num_kv_heads or q.shape[2] != c.head_dim:
+        raise ValueError("q must be [total_q, Hq, D] with Hq a multiple of the cache's heads and its D")
+    total, hq, d = q.shape
+    if out is None:
+        out = torch.empty((total, hq, d), dtype=out_dtype, device=q.device)
+    if out.dtype not in _DT or not out.is_contiguous() or out.shape != q.shape:
+        raise ValueError("out must be contiguous [total_q, Hq, D] of float32 or q's type")
+    ws = _workspace(lambda: varlen_workspace_size(B, hq, c.num_kv_heads, d, q.device.index), workspace, q.device)
+    check(lib().pkv_attn_varlen_int8(_ptr(q), _row_stride(q, "q") if total else hq * d, ctypes.byref(c), _ptr(block_tables),
+                                     block_tables.shape[1], _ptr(cu_seqlens_q), _ptr(seq_lens), B, total, int(max_q_len),
+                                     hq, float(scale), 1 if causal else 0, int(window), _ptr(out), _DT[out.dtype],
+                                     _ptr(ws), ws.numel() * ws.element_size(), _ptr(err), _stream(stream)))
     return out
 
 

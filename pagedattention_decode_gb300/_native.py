@@ -79,6 +79,8 @@ SIGNATURES = {
     "pkv_write_kv_int8": (_i32, [_vp, _vp, _i64, _vp, _i32, _P(PkvCacheI8), _vp, _vp]),
     "pkv_attn_decode_int8": (_i32, [_vp, _i64, _P(PkvCacheI8), _vp, _i32, _vp, _i32, _i32, _f32, _i32, _vp, _i32,
                                     _vp, _sz, _vp, _vp]),
+    "pkv_attn_varlen_int8": (_i32, [_vp, _i64, _P(PkvCacheI8), _vp, _i32, _vp, _vp, _i32, _i32, _i32, _i32,
+                                    _f32, _i32, _i32, _vp, _i32, _vp, _sz, _vp, _vp]),
     "pkv_attn_decode_weights_workspace_size": (_i32, [_i32, _i32, _i32, _i32, _i64, _i32, _P(_sz)]),
     "pkv_attn_decode_weights": (_i32, [_vp, _i64, _P(PkvCache), _vp, _i32, _vp, _i32, _i32, _f32, _i32, _vp, _i64,
                                        _i64, _vp, _i32, _vp, _sz, _vp, _vp]),

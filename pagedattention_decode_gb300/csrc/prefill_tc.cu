@@ -45,6 +45,7 @@
 #include <cuda.h>
 
 #include <cstring>
+#include <type_traits>
 
 #include "launch.h"
 #include "ptx.cuh"
@@ -84,6 +85,8 @@ struct TcParams {
     int32_t box_rows; // rows per K/V TMA box: 128, 64, 32 or 16, a divisor of block_size
     int32_t num_seqs;
     int32_t out_tma;  // the output map is valid: whole warps' rows leave by TMA stores
+    const int8_t *kq, *vq;  // int8 cache: code pools [num_blocks * block_size, hkv, D], scales [num_blocks, hkv]
+    const float *k_scale, *v_scale;
 };
 
 // UMMA shared-memory descriptor, 128-byte swizzle (sm_100 family layout:
@@ -217,6 +220,54 @@ __device__ __forceinline__ void st_shared_u4(uint32_t addr, uint32_t a, uint32_t
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// int8 codes as 16-bit values, exactly.  `x` holds four codes; `sel` (0x4140 or
+// 0x4342) names the pair, as bytes under zero bytes.
+template <typename T>
+__device__ __forceinline__ uint32_t code_pair(uint32_t x, uint32_t sel);
+
+// fp16: code + 128 under the exponent of 1024, minus 1152.
+template <>
+__device__ __forceinline__ uint32_t code_pair<__half>(uint32_t x, uint32_t sel) {
+    const uint32_t h = __byte_perm(x ^ 0x80808080u, 0x64646464u, sel);
+    const __half2 v = __hsub2(*reinterpret_cast<const __half2 *>(&h),
+                              __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480)));
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+// bf16 has eight significant bits: the code's low seven bits under the
+// exponent of 128, plus -128, or -256 where the sign bit is set (the sign bit
+// is bit 7 of the constant's mantissa field: one logic operation makes it).
+template <>
+__device__ __forceinline__ uint32_t code_pair<__nv_bfloat16>(uint32_t x, uint32_t sel) {
+    const uint32_t w = __byte_perm(x, 0u, sel);
+    const uint32_t a = (w & 0x007F007Fu) | 0x43004300u, b = (w & 0x00800080u) | 0xC300C300u;
+    const __nv_bfloat162 v = __hadd2(*reinterpret_cast<const __nv_bfloat162 *>(&a), *reinterpret_cast<const __nv_bfloat162 *>(&b));
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+// 16 codes (16 consecutive dims of a token row) into a tile of 128-byte-swizzled
+// rows of 64 dims: two 16-byte chunks.  The eight lanes of a store phase hold
+// one row; those of the second half of D write their odd chunk first, so the
+// phase covers eight distinct chunks of the banks.
+template <typename T>
+__device__ __forceinline__ void store_codes(uint32_t tile, int half_bytes, int row, int col, const uint4 &v) {
+    uint4 lo, hi;
+    lo.x = code_pair<T>(v.x, 0x4140u);
+    lo.y = code_pair<T>(v.x, 0x4342u);
+    lo.z = code_pair<T>(v.y, 0x4140u);
+    lo.w = code_pair<T>(v.y, 0x4342u);
+    hi.x = code_pair<T>(v.z, 0x4140u);
+    hi.y = code_pair<T>(v.z, 0x4342u);
+    hi.z = code_pair<T>(v.w, 0x4140u);
+    hi.w = code_pair<T>(v.w, 0x4342u);
+    const bool odd = col >= 4;
+    const uint32_t base = tile + (odd ? half_bytes : 0) + row * 128;
+    const uint32_t c = (uint32_t)(col & 3) * 2, sw = (uint32_t)row & 7;
+    const uint4 first = odd ? hi : lo, second = odd ? lo : hi;
+    st_shared_u4(base + (((c + odd) ^ sw) << 4), first.x, first.y, first.z, first.w);
+    st_shared_u4(base + (((c + !odd) ^ sw) << 4), second.x, second.y, second.z, second.w);
+}
+
 }  // namespace
 
 template <int D>
@@ -233,10 +284,17 @@ __host__ __device__ constexpr int prefill_stages() {  // stages of the K ring an
 // warps spill 72 bytes (loads) in their step loop; at 72 / 216 the producer
 // and MMA warps spill 96 bytes and the softmax 28 more.  88 / 208 took the
 // mixed step's prefill chunks from 1,075 to 1,121 TFLOP/s (A/B on one box).
-constexpr int kThreads = 384;
-constexpr int kRegsLow = 88;
-constexpr int kRegsHigh = 208;
-constexpr int kRegsAtLaunchMin = (128 * kRegsLow + 256 * kRegsHigh + kThreads - 1) / kThreads;
+//
+// int8 caches add a warpgroup that converts codes (512 threads, 128 registers
+// each at launch): 64 + 2 x 184 + 80 = 4 x 128.
+template <bool I8>
+struct Regs {
+    static constexpr int kThreads = I8 ? 512 : 384;
+    static constexpr int kLow = I8 ? 64 : 88;
+    static constexpr int kHigh = I8 ? 184 : 208;
+    static constexpr int kConv = 80;
+    static constexpr int kAtLaunchMin = (128 * (kLow + (I8 ? kConv : 0)) + 256 * kHigh + kThreads - 1) / kThreads;
+};
 // Epilogue staging: each softmax warp passes 16 columns of its 32 O rows
 // through shared memory (row stride 20 floats: conflict-free 16-byte
 // accesses), so the global stores cover 8 rows x 64 contiguous bytes per
@@ -252,8 +310,17 @@ struct TcItem {
     int s, kvh, q_begin, q_len, kv_len, q00, j_first, nt0, nt1;
 };
 
-template <int D, typename T>
-__global__ void __launch_bounds__(kThreads, 1)
+// I8: the pools hold int8 codes with a scale per block and KV head.  The
+// products run on the codes, which are exact as 16-bit values: K in the query's
+// type, V in bf16.  Warps 12-15 read the codes through the block table,
+// convert them in registers and write the swizzled tiles that TMA writes
+// otherwise (8 loads in flight per thread, each register reloaded as soon as
+// its codes are converted), and leave the tile's 8 + 8 scales in a ring of
+// their own.  The softmax warps multiply the scores by their block's K scale
+// in binary32 and the weights by its V scale before they are split into a
+// bf16 hi + lo pair, whose exponent range holds any scale.
+template <int D, typename T, bool I8 = false>
+__global__ void __launch_bounds__(Regs<I8>::kThreads, 1)
     prefill_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
                       const __grid_constant__ CUtensorMap tmv, const __grid_constant__ CUtensorMap tmo,
                       const TcParams p) {
@@ -264,18 +331,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int KVHALF = kTok * 128;           // bytes of 128 tokens x 64 dims
     constexpr int KVSTAGE = HALVES * KVHALF;     // one K (or V) tile
     constexpr bool BF = IsBf16<T>::value;
+    using TP = std::conditional_t<I8, __nv_bfloat16, T>;  // the type of P and V in P V
     // P enters P V as a 16-bit operand.  fp16 keeps 11 significant bits of each
     // p in [0, 2^15] (relative error <= 2^-12, far inside the 2e-3 gate); bf16
     // keeps only 8, so there P is split into hi + lo halves and P V takes two
     // MMAs per K step.  P of keys 32c .. 32c + 31 lies in TMEM columns
     // 16c .. 16c + 15 (fp16), or hi in 32c .. 32c + 15 and lo in 32c + 16 ..
     // 32c + 31 (bf16): columns whose scores have already been read.
-    constexpr bool LO = BF;
+    constexpr bool LO = BF || I8;
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t bars[2 + 4 * S + 3 * kTiles + 4 + 1];
     __shared__ TcItem s_item[2];
     __shared__ uint32_t s_tmem;
     __shared__ volatile int s_abort;
+    // int8: scale * log2(e) * K scale and V scale of the 16-token sub-blocks of a
+    // step, slot = step % 4.  The fill of step g + 4 follows the release of K
+    // stage g + 2, whose score MMAs follow the softmax of step g + 1.
+    __shared__ __align__(16) float s_scales[I8 ? 4 : 1][16];
     uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t *sq = base;
     uint8_t *sk = base + kTiles * QTILE;
@@ -305,9 +377,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(q_full, 1);
         mbar_init(q_empty, 1);
         for (int i = 0; i < S; ++i) {
-            mbar_init(&k_full[i], 1);
+            mbar_init(&k_full[i], I8 ? 4 : 1);  // the producer's bytes, or the four converting warps
             mbar_init(&k_empty[i], 1);
-            mbar_init(&v_full[i], 1);
+            mbar_init(&v_full[i], I8 ? 4 : 1);
             mbar_init(&v_empty[i], 1);
         }
         for (int u = 0; u < kTiles; ++u) {
@@ -317,7 +389,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&item_full[i], 1);
-            mbar_init(&item_empty[i], 1 + 2 * 4);  // the MMA warp and the eight softmax warps
+            mbar_init(&item_empty[i], 1 + 2 * 4 + (I8 ? 4 : 0));  // the MMA, softmax (and converting) warps
         }
         mbar_init(fin, 1);
         fence_barrier_init();
@@ -340,15 +412,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         return (kv_hi + kTok - 1) / kTok - it.j_first;
     };
     if (warp < 4) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLow));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<I8>::kLow));
     if (warp == 0) {
         // ===== producer: finds the items, then Q of both tiles and the K and V tiles of each =====
         const uint64_t pol_q = policy_evict_first();
         const uint64_t pol_kv = policy_evict_last();  // re-read by the other q tiles of the chunk
         if (lane == 0) {
             prefetch_tensormap(&tmq);
-            prefetch_tensormap(&tmk);
-            prefetch_tensormap(&tmv);
+            if constexpr (!I8) {
+                prefetch_tensormap(&tmk);
+                prefetch_tensormap(&tmv);
+            }
         }
         const int box = p.box_rows;
         const int32_t *tables = p.tables;
@@ -448,59 +522,61 @@ __global__ void __launch_bounds__(kThreads, 1)
                             (item.kvh * G + g) * HALVES + half, item.q_begin + item.q00 + u * R, pol_q);
             }
             ++q_issued;
-            // K and V tiles: a tile has at most (128 / 16) * HALVES <= 16 boxes:
-            // lane t issues box t of K and of V (sub-block t / HALVES, half t %
-            // HALVES).  Its block-table entry is read one step ahead.
-            const int32_t *trow = tables + (int64_t)item.s * p.max_blocks;
-            auto boxes_of = [&](int j) {
-                const int nvalid = min(kTok, item.kv_len - (item.j_first + j) * kTok);
-                return ((nvalid + box - 1) / box) * HALVES;
-            };
-            auto lookup = [&](int j) -> int {
-                if (j >= nt || lane >= boxes_of(j)) return 0;
-                const int tok = (item.j_first + j) * kTok + (lane / HALVES) * box;
-                return trow[tok / p.block_size];
-            };
-            int phys_next = lookup(0);
-            for (int j = 0; j < nt; ++j, ++gs) {
-                const int stage = gs % S;
-                int phys = phys_next;
-                phys_next = lookup(j + 1);
-                const int nbox = boxes_of(j);
-                const int t0 = (item.j_first + j) * kTok;
-                int row = 0;
-                if (lane < nbox) {
-                    const int tok = t0 + (lane / HALVES) * box;  // box | block_size: a box never leaves its block
-                    const int lb = tok / p.block_size;
-                    if (phys < 0 || phys >= p.num_blocks) {
-                        set_err(p.err, PKV_DEVERR_BLOCK);
-                        phys = 0;
+            if constexpr (!I8) {
+                // K and V tiles: a tile has at most (128 / 16) * HALVES <= 16 boxes:
+                // lane t issues box t of K and of V (sub-block t / HALVES, half t %
+                // HALVES).  Its block-table entry is read one step ahead.
+                const int32_t *trow = tables + (int64_t)item.s * p.max_blocks;
+                auto boxes_of = [&](int j) {
+                    const int nvalid = min(kTok, item.kv_len - (item.j_first + j) * kTok);
+                    return ((nvalid + box - 1) / box) * HALVES;
+                };
+                auto lookup = [&](int j) -> int {
+                    if (j >= nt || lane >= boxes_of(j)) return 0;
+                    const int tok = (item.j_first + j) * kTok + (lane / HALVES) * box;
+                    return trow[tok / p.block_size];
+                };
+                int phys_next = lookup(0);
+                for (int j = 0; j < nt; ++j, ++gs) {
+                    const int stage = gs % S;
+                    int phys = phys_next;
+                    phys_next = lookup(j + 1);
+                    const int nbox = boxes_of(j);
+                    const int t0 = (item.j_first + j) * kTok;
+                    int row = 0;
+                    if (lane < nbox) {
+                        const int tok = t0 + (lane / HALVES) * box;  // box | block_size: a box never leaves its block
+                        const int lb = tok / p.block_size;
+                        if (phys < 0 || phys >= p.num_blocks) {
+                            set_err(p.err, PKV_DEVERR_BLOCK);
+                            phys = 0;
+                        }
+                        row = phys * p.block_size + (tok - lb * p.block_size);
                     }
-                    row = phys * p.block_size + (tok - lb * p.block_size);
+                    const uint32_t dst_off =
+                        (uint32_t)(stage * KVSTAGE + (lane % HALVES) * KVHALF + (lane / HALVES) * box * 128);
+                    int okw = 1;
+                    if (lane == 0) okw = wait_phase(&k_empty[stage], ((gs / S) & 1) ^ 1, &s_abort);
+                    if (!__shfl_sync(0xffffffffu, okw, 0)) {
+                        ok = false;
+                        break;
+                    }
+                    if (lane == 0) mbar_arrive_expect_tx(&k_full[stage], (uint32_t)(nbox * box * 128));
+                    __syncwarp();
+                    if (lane < nbox)
+                        tma_load_3d(sk + dst_off, &tmk, &k_full[stage], 0, item.kvh * HALVES + lane % HALVES, row, pol_kv);
+                    ++issued_k;
+                    if (lane == 0) okw = wait_phase(&v_empty[stage], ((gs / S) & 1) ^ 1, &s_abort);
+                    if (!__shfl_sync(0xffffffffu, okw, 0)) {
+                        ok = false;
+                        break;
+                    }
+                    if (lane == 0) mbar_arrive_expect_tx(&v_full[stage], (uint32_t)(nbox * box * 128));
+                    __syncwarp();
+                    if (lane < nbox)
+                        tma_load_3d(sv + dst_off, &tmv, &v_full[stage], 0, item.kvh * HALVES + lane % HALVES, row, pol_kv);
+                    ++issued_v;
                 }
-                const uint32_t dst_off =
-                    (uint32_t)(stage * KVSTAGE + (lane % HALVES) * KVHALF + (lane / HALVES) * box * 128);
-                int okw = 1;
-                if (lane == 0) okw = wait_phase(&k_empty[stage], ((gs / S) & 1) ^ 1, &s_abort);
-                if (!__shfl_sync(0xffffffffu, okw, 0)) {
-                    ok = false;
-                    break;
-                }
-                if (lane == 0) mbar_arrive_expect_tx(&k_full[stage], (uint32_t)(nbox * box * 128));
-                __syncwarp();
-                if (lane < nbox)
-                    tma_load_3d(sk + dst_off, &tmk, &k_full[stage], 0, item.kvh * HALVES + lane % HALVES, row, pol_kv);
-                ++issued_k;
-                if (lane == 0) okw = wait_phase(&v_empty[stage], ((gs / S) & 1) ^ 1, &s_abort);
-                if (!__shfl_sync(0xffffffffu, okw, 0)) {
-                    ok = false;
-                    break;
-                }
-                if (lane == 0) mbar_arrive_expect_tx(&v_full[stage], (uint32_t)(nbox * box * 128));
-                __syncwarp();
-                if (lane < nbox)
-                    tma_load_3d(sv + dst_off, &tmv, &v_full[stage], 0, item.kvh * HALVES + lane % HALVES, row, pol_kv);
-                ++issued_v;
             }
         }
         if (!ok && lane == 0) {
@@ -521,7 +597,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             return __all_sync(0xffffffffu, wait_phase(bar, parity, &s_abort));
         };
         const uint32_t idS = idesc_f16(BF ? 1 : 0, 0, 128, kTok);
-        const uint32_t idPV = idesc_f16(BF ? 1 : 0, 1, 128, D);
+        const uint32_t idPV = idesc_f16(BF || I8 ? 1 : 0, 1, 128, D);
         const uint32_t sq_a = smem_u32(sq), sk_a = smem_u32(sk), sv_a = smem_u32(sv);
         // g: ring position of the K / V step
         auto issue_s = [&](int u, int g) {
@@ -593,7 +669,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t ph = (uint32_t)(tb[u] + j) & 1;
                     ok = wait(p_full(u), ph);
                     // the last step's V rows past kv_len are cleared by tile zt
-                    if (ok && u != zt && last_partial) ok = wait(p_full(zt), (uint32_t)(tb[zt] + j) & 1);
+                    if constexpr (!I8) {
+                        if (ok && u != zt && last_partial) ok = wait(p_full(zt), (uint32_t)(tb[zt] + j) & 1);
+                    }
                     if (!ok) continue;
                     tc_fence_after();
                     issue_pv(u, g, j == 0);
@@ -622,8 +700,94 @@ __global__ void __launch_bounds__(kThreads, 1)
             set_err(p.err, PKV_DEVERR_TIMEOUT);
         }
     }
+    } else if (I8 && warp >= 12) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<I8>::kConv));
+        // ===== int8: codes to 16-bit tiles =====
+        // thread = 16 codes (col) of row r16 of every 16-token sub-block of a tile
+        const int col = tid & 7, r16 = (tid & 127) >> 3;
+        const int64_t pitch = (int64_t)p.hkv * D;
+        const uint32_t sk_a = smem_u32(sk), sv_a = smem_u32(sv);
+        constexpr int SUBS = kTok / 16;
+        int gs = 0;  // ring position
+        bool ok = true;
+        for (int it = 0; ok; ++it) {
+            ok = __all_sync(0xffffffffu, wait_phase(&item_full[it & 1], (it >> 1) & 1, &s_abort));
+            if (!ok) break;
+            const TcItem item = s_item[it & 1];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&item_empty[it & 1]);
+            if (item.nt0 < 0) break;
+            const int nt = max(item.nt0, item.nt1);
+            const int32_t *trow = p.tables + (int64_t)item.s * p.max_blocks;
+            const int64_t off = (int64_t)item.kvh * D + (int64_t)r16 * pitch + col * 16;
+            // the first key of any of the item's rows (a window): earlier sub-blocks are not read
+            const int lim_first = p.causal ? item.kv_len - item.q_len + item.q00 : item.kv_len - 1;
+            const int first_key = p.window > 0 ? lim_first - p.window + 1 : 0;
+            // lane i < 8: block and pool row of sub-block i of step j, -1 where no row of the item has a key
+            int phys = -1, row = -1;
+            auto lookup = [&](int j) {
+                phys = row = -1;
+                const int tok = (item.j_first + j) * kTok + lane * 16;
+                if (j >= nt || lane >= SUBS || tok >= item.kv_len || tok + 15 < first_key) return;
+                const int lb = tok / p.block_size;
+                phys = trow[lb];
+                if (phys < 0 || phys >= p.num_blocks) {
+                    set_err(p.err, PKV_DEVERR_BLOCK);
+                    phys = 0;
+                }
+                row = phys * p.block_size + (tok - lb * p.block_size);
+            };
+            uint4 r[SUBS];
+            auto load = [&](const int8_t *pool, int i) {
+                const int rr = __shfl_sync(0xffffffffu, row, i);
+                r[i] = rr >= 0 ? __ldg(reinterpret_cast<const uint4 *>(pool + rr * pitch + off)) : make_uint4(0u, 0u, 0u, 0u);
+            };
+            lookup(0);
+#pragma unroll
+            for (int i = 0; i < SUBS; ++i) load(p.kq, i);
+            for (int j = 0; j < nt; ++j, ++gs) {
+                const int stage = gs % S;
+                const uint32_t free_parity = ((gs / S) & 1) ^ 1;
+                float ks = 0.f, vs = 0.f;
+                if (warp == 12 && lane < SUBS && phys >= 0) {
+                    ks = p.k_scale[(int64_t)phys * p.hkv + item.kvh] * p.scale_log2;
+                    vs = p.v_scale[(int64_t)phys * p.hkv + item.kvh];
+                }
+                ok = __all_sync(0xffffffffu, wait_phase(&k_empty[stage], free_parity, &s_abort));
+                if (!ok) break;
+                if (warp == 12 && lane < SUBS) {
+                    s_scales[I8 ? gs & 3 : 0][lane] = ks;
+                    s_scales[I8 ? gs & 3 : 0][8 + lane] = vs;
+                }
+#pragma unroll
+                for (int i = 0; i < SUBS; ++i) {
+                    const uint4 v = r[i];
+                    load(p.vq, i);
+                    store_codes<T>(sk_a + stage * KVSTAGE, KVHALF, i * 16 + r16, col, v);
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&k_full[stage]);
+                lookup(j + 1);
+                ok = __all_sync(0xffffffffu, wait_phase(&v_empty[stage], free_parity, &s_abort));
+                if (!ok) break;
+#pragma unroll
+                for (int i = 0; i < SUBS; ++i) {
+                    const uint4 v = r[i];
+                    load(p.kq, i);
+                    store_codes<TP>(sv_a + stage * KVSTAGE, KVHALF, i * 16 + r16, col, v);
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&v_full[stage]);
+            }
+        }
+        if (!ok && lane == 0) {
+            s_abort = 1;
+            set_err(p.err, PKV_DEVERR_TIMEOUT);
+        }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsHigh));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Regs<I8>::kHigh));
         // ===== softmax + epilogue: warps 4-7 tile 0, warps 8-11 tile 1, one M row per thread =====
         const int u = (warp - 4) >> 2;
         const int qw = warp & 3;  // a warp reaches TMEM lanes 32 * (warp % 4) .. + 31
@@ -660,7 +824,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // the step whose V rows past kv_len this tile clears (the item's last
             // step, when it is partial and this tile is the first to read it), or -1
             const int zt = nt0 == nt ? 0 : 1;
-            const int jzero = (u == zt && (j_first + nt) * kTok > item.kv_len) ? nt - 1 : -1;
+            const int jzero = (!I8 && u == zt && (j_first + nt) * kTok > item.kv_len) ? nt - 1 : -1;
             float m_used = -INFINITY, lsum = 0.f;
             for (int j = 0; j < ntu; ++j) {
                 const int gpos = gcs + j;
@@ -682,6 +846,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int c0 = 0; c0 < kTok; c0 += 32)
                     tmem_ld32(trow_addr + c0, *reinterpret_cast<uint32_t(*)[32]>(&sr[c0]));
                 tmem_wait_ld();
+                // int8: a masked step's scores take their K scale here (a scale of 0
+                // would turn a masked -inf into NaN), a whole step's below
+                const float *scl = s_scales[I8 ? gpos & 3 : 0];
+                if constexpr (I8) {
+                    if (!whole) {
+#pragma unroll
+                        for (int c = 0; c < kTok; ++c) sr[c] = __float_as_uint(__uint_as_float(sr[c]) * scl[c / 16]);
+                    }
+                }
+                auto k_mul = [&](int c) -> float { return whole ? scl[c / 16] : 1.f; };
                 if (!whole) {
                     // keys t0 + c with c > lim - t0 (causal limit) or c < lo - t0
                     // (window start) are invisible; the start only matters on
@@ -700,14 +874,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // independent chains of three-input maxima
                 auto row_max = [&]() -> float {
                     float pm[8];
+                    if constexpr (I8) {  // taken on few steps: the products one by one
+                        pm[0] = -INFINITY;
     #pragma unroll
-                    for (int v = 0; v < 8; ++v) pm[v] = fmaxf(__uint_as_float(sr[v]), __uint_as_float(sr[8 + v]));
-    #pragma unroll
-                    for (int c = 16; c < kTok; c += 16)
-    #pragma unroll
-                        for (int v = 0; v < 8; ++v)
-                            pm[v] = fmax3(pm[v], __uint_as_float(sr[c + v]), __uint_as_float(sr[c + 8 + v]));
-                    return fmaxf(fmax3(pm[0], pm[1], pm[2]), fmax3(pm[3], pm[4], fmax3(pm[5], pm[6], pm[7]))) * sl;
+                        for (int c = 0; c < kTok; ++c) pm[0] = fmaxf(pm[0], __uint_as_float(sr[c]) * k_mul(c));
+                        return pm[0];
+                    } else {
+        #pragma unroll
+                        for (int v = 0; v < 8; ++v) pm[v] = fmaxf(__uint_as_float(sr[v]), __uint_as_float(sr[8 + v]));
+        #pragma unroll
+                        for (int c = 16; c < kTok; c += 16)
+        #pragma unroll
+                            for (int v = 0; v < 8; ++v)
+                                pm[v] = fmax3(pm[v], __uint_as_float(sr[c + v]), __uint_as_float(sr[c + 8 + v]));
+                        return fmaxf(fmax3(pm[0], pm[1], pm[2]), fmax3(pm[3], pm[4], fmax3(pm[5], pm[6], pm[7]))) * sl;
+                    }
                 };
                 // The running max m_used is taken from the row's first tile with
                 // a visible key and is moved only when p would leave the range
@@ -734,17 +915,32 @@ __global__ void __launch_bounds__(kThreads, 1)
     #pragma unroll
                     for (int c0 = 0; c0 < kTok; c0 += 32) {
                         uint32_t ph[16], pl[16];
+                        float2 kv2[2][2];  // int8: (K factor, V scale) of the chunk's two sub-blocks
+                        if constexpr (I8) {
+    #pragma unroll
+                            for (int b = 0; b < 2; ++b) {
+                                const float kf = k_mul(c0 + 16 * b), vf = scl[8 + c0 / 16 + b];
+                                kv2[b][0] = make_float2(kf, kf);
+                                kv2[b][1] = make_float2(vf, vf);
+                            }
+                        }
     #pragma unroll
                         for (int c = 0; c < 32; c += 2) {
                             const float2 x = __ffma2_rn(
-                                make_float2(__uint_as_float(sr[c0 + c]), __uint_as_float(sr[c0 + c + 1])), sl2, nm2);
-                            const float p0 = fast_exp2(x.x), p1 = fast_exp2(x.y);
+                                make_float2(__uint_as_float(sr[c0 + c]), __uint_as_float(sr[c0 + c + 1])),
+                                I8 ? kv2[c / 16][0] : sl2, nm2);
+                            float p0 = fast_exp2(x.x), p1 = fast_exp2(x.y);
                             ps[(c >> 1) & 3] = __fadd2_rn(ps[(c >> 1) & 3], make_float2(p0, p1));
-                            const uint32_t h = pack2<T>(p0, p1);
+                            if constexpr (I8) {
+                                const float2 pv = __fmul2_rn(make_float2(p0, p1), kv2[c / 16][1]);
+                                p0 = pv.x;
+                                p1 = pv.y;
+                            }
+                            const uint32_t h = pack2<TP>(p0, p1);
                             ph[c / 2] = h;
                             if (LO) {
-                                const float2 hf = unpack2<T>(h);
-                                pl[c / 2] = pack2<T>(p0 - hf.x, p1 - hf.y);
+                                const float2 hf = unpack2<TP>(h);
+                                pl[c / 2] = pack2<TP>(p0 - hf.x, p1 - hf.y);
                             }
                         }
                         if (LO) {
@@ -950,7 +1146,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-template <int D, typename T>
+template <int D, typename T, bool I8 = false>
 static pkv_status launch_prefill_tc_t(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv,
                                       const CUtensorMap &mo, const TcParams &p, int num_seqs, cudaStream_t stream) {
     constexpr int HALVES = D / 64;
@@ -959,7 +1155,7 @@ static pkv_status launch_prefill_tc_t(const CUtensorMap &mq, const CUtensorMap &
     // epilogue staging rows
     const int smem = kTiles * HALVES * 128 * 128 + 2 * prefill_stages<D>() * HALVES * kTok * 128 + 1024 + 4096 +
                      kStageBytes;
-    auto kern = prefill_tc_kernel<D, T>;
+    auto kern = prefill_tc_kernel<D, T, I8>;
     static std::atomic<uint64_t> smem_set{0};
     pkv_status st = set_smem_once(reinterpret_cast<const void *>(kern), smem, &smem_set);
     if (st != PKV_OK) return st;
@@ -970,16 +1166,17 @@ static pkv_status launch_prefill_tc_t(const CUtensorMap &mq, const CUtensorMap &
     const int64_t most_items = (int64_t)p.q_tiles * num_seqs * p.hkv;
     dim3 grid((unsigned)(most_items < sms ? most_items : sms));
     // the register re-balancing inside the kernel needs at least
-    // kRegsAtLaunchMin registers per thread at launch, or it would wait forever
+    // Regs::kAtLaunchMin registers per thread at launch, or it would wait forever
     static std::atomic<int> regs{0};
     if (regs.load() == 0) {
         cudaFuncAttributes fa{};
         PKV_CUDA_TRY(cudaFuncGetAttributes(&fa, reinterpret_cast<const void *>(kern)));
         regs.store(fa.numRegs);
     }
-    PKV_CHECK_ARG(regs.load() >= kRegsAtLaunchMin, PKV_ERR_UNSUPPORTED,
-                  "prefill kernel built with %d registers per thread, needs >= %d", regs.load(), kRegsAtLaunchMin);
-    return launch_pdl(kern, grid, dim3(kThreads), (size_t)smem, stream, mq, mk, mv, mo, p);
+    PKV_CHECK_ARG(regs.load() >= Regs<I8>::kAtLaunchMin, PKV_ERR_UNSUPPORTED,
+                  "prefill kernel built with %d registers per thread, needs >= %d", regs.load(),
+                  Regs<I8>::kAtLaunchMin);
+    return launch_pdl(kern, grid, dim3(Regs<I8>::kThreads), (size_t)smem, stream, mq, mk, mv, mo, p);
 }
 
 // Prefill chunks of a varlen call on tcgen05 (rows of q_len == 1 are left to the decode kernel).
@@ -1038,6 +1235,50 @@ pkv_status run_prefill_tc(const void *q, int64_t q_stride, const pkv_cache *cach
                   : launch_prefill_tc_t<64, __half>(mq, mk, mv, mo, p, num_seqs, stream);
     return bf ? launch_prefill_tc_t<128, __nv_bfloat16>(mq, mk, mv, mo, p, num_seqs, stream)
               : launch_prefill_tc_t<128, __half>(mq, mk, mv, mo, p, num_seqs, stream);
+}
+
+// The same over an int8 cache (head_dim 128).
+pkv_status run_prefill_i8(const void *q, int64_t q_stride, const pkv_cache_i8 *cache, const int32_t *tables,
+                          int32_t max_blocks, const int32_t *cu_q, const int32_t *seq_lens, int32_t num_seqs,
+                          int32_t total_q, int32_t max_q_len, int32_t num_q_heads, float scale, int32_t causal,
+                          int32_t window, void *out, int32_t out_dtype, int32_t *err_word, cudaStream_t stream) {
+    PKV_CHECK_ARG(aligned16(q) && (q_stride * 2) % 16 == 0, PKV_ERR_INVALID_ARG,
+                  "pkv_attn_varlen_int8: q and its row stride must be 16-byte aligned for prefill chunks");
+    TcParams p{};
+    p.tables = tables;
+    p.max_blocks = max_blocks;
+    p.seq_lens = seq_lens;
+    p.cu_q = cu_q;
+    p.num_blocks = cache->num_blocks;
+    p.block_size = cache->block_size;
+    p.hkv = cache->num_kv_heads;
+    p.group = num_q_heads / cache->num_kv_heads;
+    p.causal = causal ? 1 : 0;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    p.out = out;
+    p.out_f32 = out_dtype == PKV_F32;
+    p.err = err_word;
+    p.window = window > 0 ? window : 0;
+    const int rows = 128 / p.group;
+    p.q_tiles = (max_q_len + kTiles * rows - 1) / (kTiles * rows);
+    p.num_seqs = num_seqs;
+    p.q = q;
+    p.q_stride = q_stride;
+    p.kq = cache->k;
+    p.vq = cache->v;
+    p.k_scale = cache->k_scale;
+    p.v_scale = cache->v_scale;
+    CUtensorMap mq, mo, none;
+    memset(&none, 0, sizeof(none));
+    pkv_status st = encode_q_map(&mq, q, q_stride, total_q, num_q_heads, cache->head_dim, rows, cache->dtype);
+    if (st != PKV_OK) return st;
+    const int wrows = rows < 32 ? rows : 32;
+    st = encode_out_map(&mo, out, total_q, num_q_heads, cache->head_dim, out_dtype, out_dtype == PKV_F32 ? 16 : 32, wrows,
+                        32 / wrows);
+    if (st != PKV_OK) return st;
+    p.out_tma = 1;
+    return cache->dtype == PKV_BF16 ? launch_prefill_tc_t<128, __nv_bfloat16, true>(mq, none, none, mo, p, num_seqs, stream)
+                                    : launch_prefill_tc_t<128, __half, true>(mq, none, none, mo, p, num_seqs, stream);
 }
 
 }  // namespace pkv

@@ -20,8 +20,8 @@ pkv_status run_decode(const void *q, int64_t q_stride, const pkv_cache *cache, c
                       int32_t max_blocks, const int32_t *seq_lens, const int32_t *cu_q, int32_t num_seqs,
                       int32_t num_q_heads, float scale, void *out, int32_t out_dtype, void *workspace,
                       size_t workspace_bytes, int32_t *err_word, cudaStream_t stream);
-pkv_status decode_workspace_size(int32_t num_seqs, int32_t num_q_heads, int32_t hkv, int32_t head_dim,
-                                 int32_t device, size_t *bytes);
+pkv_status decode_workspace_size_any(int32_t num_seqs, int32_t num_q_heads, int32_t hkv, int32_t head_dim,
+                                     int32_t device, size_t *bytes);
 pkv_status run_decode_window(const void *q, int64_t q_stride, const pkv_cache *cache, const int32_t *tables,
                              int32_t max_blocks, const int32_t *seq_lens, const int32_t *cu_q, int32_t num_seqs,
                              int32_t num_q_heads, float scale, int32_t window, void *out, int32_t out_dtype,
@@ -34,6 +34,19 @@ pkv_status check_attention_common(const void *q, int64_t q_stride, const pkv_cac
                                   int32_t max_blocks, const int32_t *seq_lens, int32_t num_seqs,
                                   int32_t num_q_heads, void *out, int32_t out_dtype, const char *what);
 
+pkv_status run_decode_i8(const void *q, int64_t q_stride, const pkv_cache_i8 *cache, const int32_t *tables,
+                         int32_t max_blocks, const int32_t *seq_lens, const int32_t *cu_q, int32_t num_seqs,
+                         int32_t num_q_heads, float scale, int32_t window, void *out, int32_t out_dtype,
+                         void *workspace, size_t workspace_bytes, int32_t *err_word, cudaStream_t stream);
+pkv_status run_prefill_i8(const void *q, int64_t q_stride, const pkv_cache_i8 *cache, const int32_t *tables,
+                          int32_t max_blocks, const int32_t *cu_q, const int32_t *seq_lens, int32_t num_seqs,
+                          int32_t total_q, int32_t max_q_len, int32_t num_q_heads, float scale, int32_t causal,
+                          int32_t window, void *out, int32_t out_dtype, int32_t *err_word, cudaStream_t stream);
+pkv_status check_attention_i8(const void *q, int64_t q_token_stride, const pkv_cache_i8 *cache,
+                              const int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *seq_lens,
+                              int32_t num_seqs, int32_t num_q_heads, const void *out, int32_t out_dtype,
+                              const char *what);
+
 }  // namespace pkv
 
 using namespace pkv;
@@ -44,7 +57,7 @@ pkv_status pkv_attn_varlen_workspace_size(int32_t num_seqs, int32_t num_q_heads,
                                           int32_t head_dim, int32_t device, size_t *bytes) {
     PKV_CHECK_ARG(bytes && num_seqs >= 0 && num_kv_heads > 0 && num_q_heads > 0 && head_dim > 0,
                   PKV_ERR_INVALID_ARG, "bad argument");
-    pkv_status st = decode_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, device, bytes);
+    pkv_status st = decode_workspace_size_any(num_seqs, num_q_heads, num_kv_heads, head_dim, device, bytes);
     return st == PKV_OK ? ok() : st;
 }
 
@@ -93,6 +106,29 @@ pkv_status pkv_attn_varlen_window(const void *q, int64_t q_token_stride, const p
     return varlen_impl(q, q_token_stride, cache, block_tables, max_blocks_per_seq, cu_seqlens_q, seq_lens, num_seqs,
                        total_q, max_q_len, num_q_heads, scale, causal, window, out, out_dtype, workspace,
                        workspace_bytes, err_word, stream, "pkv_attn_varlen_window");
+}
+
+pkv_status pkv_attn_varlen_int8(const void *q, int64_t q_token_stride, const pkv_cache_i8 *cache,
+                                const int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *cu_seqlens_q,
+                                const int32_t *seq_lens, int32_t num_seqs, int32_t total_q, int32_t max_q_len,
+                                int32_t num_q_heads, float scale, int32_t causal, int32_t window, void *out,
+                                int32_t out_dtype, void *workspace, size_t workspace_bytes, int32_t *err_word,
+                                pkv_stream stream) {
+    PKV_CHECK_ARG(total_q >= 0 && max_q_len >= 0, PKV_ERR_INVALID_ARG, "negative total_q or max_q_len");
+    PKV_CHECK_ARG(num_seqs >= 0, PKV_ERR_INVALID_ARG, "negative size");
+    pkv_status st = check_attention_i8(q, q_token_stride, cache, block_tables, max_blocks_per_seq, seq_lens,
+                                       total_q > 0 ? num_seqs : 0, num_q_heads, out, out_dtype, "pkv_attn_varlen_int8");
+    if (st != PKV_OK) return st;
+    if (num_seqs == 0 || total_q == 0) return ok();
+    PKV_CHECK_ARG(cu_seqlens_q, PKV_ERR_INVALID_ARG, "cu_seqlens_q is NULL");
+    PKV_CHECK_ARG(num_seqs <= 65535, PKV_ERR_UNSUPPORTED, "at most 65535 sequences per call");
+    st = run_decode_i8(q, q_token_stride, cache, block_tables, max_blocks_per_seq, seq_lens, cu_seqlens_q, num_seqs,
+                       num_q_heads, scale, window, out, out_dtype, workspace, workspace_bytes, err_word, stream);
+    if (st != PKV_OK) return st;
+    if (max_q_len <= 1) return ok();
+    st = run_prefill_i8(q, q_token_stride, cache, block_tables, max_blocks_per_seq, cu_seqlens_q, seq_lens, num_seqs,
+                        total_q, max_q_len, num_q_heads, scale, causal, window, out, out_dtype, err_word, stream);
+    return st == PKV_OK ? ok() : st;
 }
 
 }  // extern "C"
