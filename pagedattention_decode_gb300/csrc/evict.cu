@@ -8,24 +8,26 @@
 // may keep different positions while the sequence keeps one block table and
 // one length.
 //
-//  * evict_select_kernel: the n-th largest weight of a row by radix selection
-//    on the order-preserving integer image of the floats (11 + 11 + 10 bits),
-//    then one ordered pass that writes the kept positions.
+//  * evict_select_kernel: the n-th largest weight of a row by bisection on the
+//    order-preserving integer image of the floats, then one ordered pass that
+//    writes the kept positions.
 //  * evict_compact_kernel, evict_compact_i8_kernel: the moves, in place.  Row
 //    i comes from position kept[i] >= i and kept ascends, so a chunk of rows
 //    whose sources were all read can be written without touching a source of
 //    any later chunk; chunks of one (sequence, head) are taken in order, each
 //    one's loads before its stores.
+#include <cooperative_groups.h>
+
 #include "launch.h"
 #include "ptx.cuh"
 
 namespace pkv {
 
+namespace cg = cooperative_groups;
+
 namespace {
 
-constexpr int kSelThreads = 1024;
-constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kBins = 2048;
+constexpr int kSelMaxCluster = 8;  // the portable limit
 
 struct SelectParams {
     const float *w;
@@ -37,135 +39,308 @@ struct SelectParams {
     int32_t *kept;
     int32_t *new_lens;
     int32_t *err;
+    int32_t cluster;
+    int32_t run_chunks;          // chunks of 128 keys that a warp's part of the shared memory holds
 };
 
 // Integers that order as the floats do (-0 as +0), NaN above +inf.
 __device__ __forceinline__ uint32_t order_key(float f) {
     const uint32_t b = __float_as_uint(f + 0.f);
-    if (f != f) return 0xFFFFFFFEu;
-    return b & 0x80000000u ? ~b : b | 0x80000000u;
+    const uint32_t k = b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+    return f != f ? 0xFFFFFFFEu : k;
 }
 
-// Exclusive block-wide prefix of two ints per thread; totals in *ta, *tb.
-__device__ __forceinline__ void block_prefix2(int &a, int &b, int *ta, int *tb, int (*s)[kSelWarps]) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int x = a, y = b;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int u = __shfl_up_sync(0xffffffffu, x, o), v = __shfl_up_sync(0xffffffffu, y, o);
-        if (lane >= o) {
-            x += u;
-            y += v;
-        }
-    }
-    if (lane == 31) {
-        s[0][warp] = x;
-        s[1][warp] = y;
-    }
-    __syncthreads();
-    if (warp == 0) {
-        int p = s[0][lane], q = s[1][lane];
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int u = __shfl_up_sync(0xffffffffu, p, o), v = __shfl_up_sync(0xffffffffu, q, o);
-            if (lane >= o) {
-                p += u;
-                q += v;
-            }
-        }
-        s[0][lane] = p;
-        s[1][lane] = q;
-    }
-    __syncthreads();
-    a = x - a + (warp ? s[0][warp - 1] : 0);
-    b = y - b + (warp ? s[1][warp - 1] : 0);
-    *ta = s[0][kSelWarps - 1];
-    *tb = s[1][kSelWarps - 1];
-    __syncthreads();
-}
-
-// One CTA per (sequence, KV head).
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const SelectParams p) {
-    __shared__ int s_hist[kBins];
-    __shared__ int s_scan[2][kSelWarps];
-    __shared__ int s_bin, s_need;
+// A row is one (sequence, KV head).  The budget-th largest key is searched
+// between the row's extremes: a step counts the keys that reach a trial value,
+// the bracket closes on it, and when exactly `budget` keys do the search ends
+// (distinct weights: after some 8 steps for the lognormal weights of a long
+// history, 12-16 by bisection alone).  Two steps of three interpolate the
+// counts between the bracket's ends, the third halves it, which bounds the steps
+// by 3 x 32.
+//  WARPS: warps per CTA, and per row without clusters.
+//  CLUSTER: the row is split over p.cluster CTAs, which store their counts in
+//  each other's shared memory before a cluster barrier.
+//  RESIDENT: the keys stay in shared memory, and a step reads four per lane and
+//  instruction; false (more than 131,072 keys): the weights are read again in
+//  every step, from L2.
+// CTA r of a cluster takes the r-th contiguous run of positions, warp w the
+// w-th run of that, in chunks of 128, four neighbours to a lane.
+// What bounds it: integer compares and adds, which issue at half rate (a count
+// is two per key), and latency.
+template <int WARPS, bool CLUSTER, bool RESIDENT>
+__global__ void __launch_bounds__(32 * WARPS) evict_select_kernel(const SelectParams p) {
+    extern __shared__ uint4 s_keys[];
+    constexpr int TRIALS = CLUSTER ? 3 : 1;
+    __shared__ uint32_t s_part[2][WARPS];  // a sum's terms by warp; alternating buffers, one barrier a sum
+    __shared__ uint32_t s_sum[2][kSelMaxCluster];
+    __shared__ uint32_t s_try[2][CLUSTER ? WARPS : 1][4], s_tries[2][kSelMaxCluster][4];
+    __shared__ uint32_t s_at[2][WARPS];
     pdl_wait();
     pdl_trigger();
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int64_t row = blockIdx.x;
+    const int lane = threadIdx.x & 31;
+    const int warp = threadIdx.x >> 5, tid = threadIdx.x;
+    const int rank = CLUSTER ? (int)(blockIdx.x % p.cluster) : 0;
+    const int64_t row = CLUSTER ? blockIdx.x / p.cluster : blockIdx.x;
     const int64_t seq = row / p.hkv;
     const int h = (int)(row - seq * p.hkv);
     const int L = p.seq_lens[seq];
     int32_t *kept = p.kept + row * p.budget;
     const bool bad = L < 0 || L > p.max_keys;
-    if (tid == 0 && h == 0) {
+    if (tid == 0 && h == 0 && rank == 0) {
         if (bad) set_err(p.err, PKV_DEVERR_LENGTH);
         p.new_lens[seq] = bad || L < p.budget ? L : p.budget;
     }
-    if (bad || L <= p.budget) {  // nothing goes
-        for (int i = tid; i < p.budget; i += kSelThreads) kept[i] = !bad && i < L ? i : -1;
+    if (bad || L <= p.budget) {  // nothing goes (all threads of the row agree)
+        for (int i = rank * 32 * WARPS + tid; i < p.budget; i += (CLUSTER ? p.cluster : 1) * 32 * WARPS)
+            kept[i] = !bad && i < L ? i : -1;
         return;
     }
     const float *w = p.w + seq * p.seq_stride + h * p.head_stride;
     const int tail = L - p.recent;
-    auto key = [&](int t) -> uint32_t { return t < p.sink || t >= tail ? 0xFFFFFFFFu : order_key(w[t]); };
+    const int part = CLUSTER ? (L + p.cluster - 1) / p.cluster : L;
+    const int seg = ((part + WARPS - 1) / WARPS + 127) & ~127;  // a warp's run: whole chunks
+    const int64_t first = ((int64_t)rank * WARPS + warp) * seg;
+    const int a = (int)(first < L ? first : L), b = min(L, a + seg);
+    const int chunks = (b - a + 127) >> 7;
+    const bool vec = (reinterpret_cast<uintptr_t>(w) & 15) == 0;
+    auto read = [&](int c) -> uint4 {  // the lane's keys of chunk c; 0, past the run's end, reaches no trial
+        const int t = a + 128 * c + 4 * lane;
+        const int t0 = a + 128 * c;
+        if (vec && t0 >= p.sink && t0 + 128 <= min(b, tail)) {  // nothing protected, nothing past the end
+            const float4 v = *reinterpret_cast<const float4 *>(w + t);
+            return make_uint4(order_key(v.x), order_key(v.y), order_key(v.z), order_key(v.w));
+        }
+        float f[4] = {0.f, 0.f, 0.f, 0.f};
+        if (vec && t + 3 < b) {
+            const float4 v = *reinterpret_cast<const float4 *>(w + t);
+            f[0] = v.x;
+            f[1] = v.y;
+            f[2] = v.z;
+            f[3] = v.w;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (t + j < b) f[j] = w[t + j];
+        }
+        uint32_t k[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            k[j] = t + j < p.sink || t + j >= tail ? 0xFFFFFFFFu : order_key(f[j]);
+            if (t + j >= b) k[j] = 0u;
+        }
+        return make_uint4(k[0], k[1], k[2], k[3]);
+    };
+    uint4 *mine = nullptr;  // a lane reads only what it wrote
+    if constexpr (RESIDENT) {
+        mine = s_keys + warp * (p.run_chunks * 32) + lane;
+#pragma unroll 8
+        for (int c = 0; c < chunks; ++c) mine[32 * c] = read(c);
+    }
+    auto each = [&](auto &&f) {  // f(position of the lane's first key, its four keys), in order
+        if constexpr (RESIDENT) {
+#pragma unroll 4
+            for (int c = 0; c < chunks; ++c) f(a + 128 * c + 4 * lane, mine[32 * c]);
+        } else {
+            for (int c = 0; c < chunks; ++c) f(a + 128 * c + 4 * lane, read(c));
+        }
+    };
+    // sum, or minimum, of x (the same in a warp's lanes) over the row's warps
+    int round = 0;
+    auto over_row = [&](uint32_t x, auto &&reduce, uint32_t none) -> uint32_t {
+        const int buf = round++ & 1;
+        if (lane == 0) s_part[buf][warp] = x;
+        __syncthreads();
+        x = reduce(lane < WARPS ? s_part[buf][lane] : none);
+        if constexpr (CLUSTER) {
+            if (warp == 0 && lane < p.cluster) *cg::this_cluster().map_shared_rank(&s_sum[buf][rank], lane) = x;
+            cg::this_cluster().sync();
+            x = reduce(lane < p.cluster ? s_sum[buf][lane] : none);
+        }
+        return x;
+    };
+    auto sum = [](uint32_t x) { return __reduce_add_sync(0xffffffffu, x); };
+    auto least_of = [](uint32_t x) { return __reduce_min_sync(0xffffffffu, x); };
+    if constexpr (CLUSTER) cg::this_cluster().sync();  // every CTA of the row runs: its memory may be written
 
-    // the budget-th largest key, digit by digit
-    uint32_t prefix = 0, mask = 0;
-    int need = p.budget;
-#pragma unroll 1
-    for (int pass = 0; pass < 3; ++pass) {
-        const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
-        const uint32_t digits = pass == 2 ? 1023u : 2047u;
-        for (int i = tid; i < kBins; i += kSelThreads) s_hist[i] = 0;
-        __syncthreads();
-        for (int t = tid; t < L; t += kSelThreads) {
-            const uint32_t k = key(t);
-            if ((k & mask) == prefix) atomicAdd(&s_hist[(k >> shift) & digits], 1);
+    // the bracket: `budget` keys or more reach lo, fewer reach hi
+    uint32_t lo = 0xFFFFFFFFu, top = 0;
+    each([&](int, const uint4 &k) {
+        // less one, 0 (no key) is the largest; with one, 0xFFFFFFFF (a protected position) the smallest
+        lo = min(min(lo, min(k.x - 1u, k.y - 1u)), min(k.z - 1u, k.w - 1u));
+        top = max(max(top, max(k.x + 1u, k.y + 1u)), max(k.z + 1u, k.w + 1u));
+    });
+    lo = over_row(least_of(lo), least_of, 0xFFFFFFFFu) + 1u;
+    uint32_t hi = ~over_row(least_of(~top), least_of, 0xFFFFFFFFu);
+    int reach_lo = L, reach_hi = p.sink + p.recent;
+    bool exact = reach_hi == p.budget;      // exactly `budget` keys reach the bar
+    uint32_t bar = exact ? 0xFFFFFFFFu : lo;
+    for (int step = 0; !exact && hi - lo > 1u; ++step) {
+        if constexpr (CLUSTER) {
+            // the bracket in four: three counts behind one barrier (a try that falls
+            // on lo counts what lo does).  A count of 16,384 keys takes ~650 cycles of
+            // the CTA, a barrier with its exchange ~1,300: one count a step by
+            // interpolation, or seven, take as long.
+            uint32_t mid[TRIALS], cnt[TRIALS];
+#pragma unroll
+            for (int v = 0; v < TRIALS; ++v) {
+                mid[v] = lo + (uint32_t)((uint64_t)(hi - lo) * (v + 1) / (TRIALS + 1));
+                cnt[v] = 0;
+            }
+            each([&](int, const uint4 &k) {
+#pragma unroll
+                for (int v = 0; v < TRIALS; ++v) cnt[v] += (k.x >= mid[v]) + (k.y >= mid[v]) + (k.z >= mid[v]) + (k.w >= mid[v]);
+            });
+            const int buf = step & 1;
+#pragma unroll
+            for (int v = 0; v < TRIALS; ++v) {
+                cnt[v] = sum(cnt[v]);
+                if (lane == v) s_try[buf][warp][v] = cnt[v];
+            }
+            __syncthreads();
+            if (warp < TRIALS) {  // warp v: try v of this CTA, to every CTA of the row
+                const uint32_t c = sum(s_try[buf][lane][warp]);
+                if (lane < p.cluster) *cg::this_cluster().map_shared_rank(&s_tries[buf][rank][warp], lane) = c;
+            }
+            cg::this_cluster().sync();
+            uint32_t reach = 0;
+            if (lane < TRIALS)
+                for (int r = 0; r < p.cluster; ++r) reach += s_tries[buf][r][lane];
+#pragma unroll
+            for (int v = 0; v < TRIALS; ++v) cnt[v] = __shfl_sync(0xffffffffu, reach, v);
+#pragma unroll
+            for (int v = TRIALS - 1; v >= 0; --v)
+                if (cnt[v] < (uint32_t)p.budget) {
+                    hi = mid[v];
+                    reach_hi = (int)cnt[v];
+                }
+#pragma unroll
+            for (int v = 0; v < TRIALS; ++v)
+                if (cnt[v] >= (uint32_t)p.budget) {
+                    lo = mid[v];
+                    reach_lo = (int)cnt[v];
+                }
+            bar = lo;
+            exact = reach_lo == p.budget;
+        } else {
+            uint32_t mid = lo + (hi - lo) / 2;
+            if (step % 3 != 2) {
+                const float f = (float)(reach_lo - p.budget) / (float)(reach_lo - reach_hi);
+                const uint32_t d = (uint32_t)fminf((float)(hi - lo) * f, 4294967040.f);
+                mid = lo + min(max(d, 1u), hi - lo - 1u);
+            }
+            uint32_t c0 = 0, c1 = 0;
+            each([&](int, const uint4 &k) {
+                c0 += k.x >= mid;
+                c1 += k.y >= mid;
+                c0 += k.z >= mid;
+                c1 += k.w >= mid;
+            });
+            const int reach = (int)over_row(sum(c0 + c1), sum, 0u);
+            exact = reach == p.budget;
+            if (reach >= p.budget) {
+                bar = lo = mid;
+                reach_lo = reach;
+            } else {
+                hi = mid;
+                reach_hi = reach;
+            }
         }
-        __syncthreads();
-        // thread i holds bins 2047 - 2i and 2046 - 2i: an exclusive prefix counts the keys above
-        const int hi = kBins - 1 - 2 * tid;
-        const int c0 = s_hist[hi], c1 = s_hist[hi - 1];
-        int above = c0 + c1, dummy = 0, t0, t1;
-        block_prefix2(above, dummy, &t0, &t1, s_scan);
-        if (above < need && need <= above + c0 + c1) {
-            const bool first = need <= above + c0;
-            s_bin = first ? hi : hi - 1;
-            s_need = need - above - (first ? 0 : c0);
-        }
-        __syncthreads();
-        prefix |= (uint32_t)s_bin << shift;
-        mask |= digits << shift;
-        need = s_need;
-        __syncthreads();
     }
-    // keys above `prefix` stay, and the first `need` of those equal to it; a
-    // warp takes a contiguous run of positions
-    const int seg = ((L + kSelWarps - 1) / kSelWarps + 31) & ~31;
-    const int a = min(L, warp * seg), b = min(L, a + seg);
-    int gt = 0, eq = 0;
-    for (int t = a + lane; t < b; t += 32) {
-        const uint32_t k = key(t);
-        gt += k > prefix;
-        eq += k == prefix;
+    // Where the search ran through, `bar` is the budget-th largest key: the
+    // `reach_hi` keys above it stay, and of those equal to it the first `need`.
+    const int need = exact ? 0 : p.budget - reach_hi;
+    uint32_t at = 0, same = 0, eq = 0;  // what lies before this warp; its own ties
+    uint32_t gt = 0;
+    each([&](int, const uint4 &k) {
+        gt += (k.x > bar) + (k.y > bar) + (k.z > bar) + (k.w > bar);
+        eq += (k.x == bar) + (k.y == bar) + (k.z == bar) + (k.w == bar);
+    });
+    gt = sum(gt);
+    eq = sum(eq);
+    if (exact) {
+        gt += eq;
+        eq = 0;
     }
-    int ta, tb;
-    block_prefix2(gt, eq, &ta, &tb, s_scan);
-    gt = __shfl_sync(0xffffffffu, gt, 0);
-    eq = __shfl_sync(0xffffffffu, eq, 0);
-    int at = gt + min(eq, need);
-    for (int t0 = a; t0 < b; t0 += 32) {
-        const int t = t0 + lane;
-        const uint32_t k = t < b ? key(t) : 0u;
-        const unsigned me = 1u << lane, below = me - 1;
-        const unsigned same = __ballot_sync(0xffffffffu, t < b && k == prefix);
-        const bool take = t < b && (k > prefix || (k == prefix && eq + __popc(same & below) < need));
-        const unsigned taken = __ballot_sync(0xffffffffu, take);
-        if (take) kept[at + __popc(taken & below)] = t;
-        at += __popc(taken);
-        eq += __popc(same);
+    if (lane == 0) {
+        s_at[0][warp] = gt;
+        s_at[1][warp] = eq;
     }
+    __syncthreads();
+    const uint32_t x = lane < WARPS ? s_at[0][lane] : 0u, y = lane < WARPS ? s_at[1][lane] : 0u;
+    at = sum(lane < warp ? x : 0u);
+    same = sum(lane < warp ? y : 0u);
+    if constexpr (CLUSTER) {
+        // two more exchanges: the earlier CTAs' totals
+        const uint32_t above = sum(x), ties = sum(y);
+        auto before = [&](uint32_t v) {
+            const int buf = round++ & 1;
+            if (warp == 0 && lane < p.cluster) *cg::this_cluster().map_shared_rank(&s_sum[buf][rank], lane) = v;
+            cg::this_cluster().sync();
+            return sum(lane < rank ? s_sum[buf][lane] : 0u);
+        };
+        at += before(above);
+        same += before(ties);
+    }
+    at += min(same, (uint32_t)need);
+    const unsigned below = (1u << lane) - 1u;
+    // the lane's chosen keys (bit j: key j) to their places
+    auto put = [&](int t, unsigned take) {
+        const unsigned m0 = __ballot_sync(0xffffffffu, take & 1u), m1 = __ballot_sync(0xffffffffu, take & 2u);
+        const unsigned m2 = __ballot_sync(0xffffffffu, take & 4u), m3 = __ballot_sync(0xffffffffu, take & 8u);
+        uint32_t i = at + __popc(m0 & below) + __popc(m1 & below) + __popc(m2 & below) + __popc(m3 & below);
+        if (take & 1u) kept[i] = t;
+        i += take & 1u;
+        if (take & 2u) kept[i] = t + 1;
+        i += take >> 1 & 1u;
+        if (take & 4u) kept[i] = t + 2;
+        i += take >> 2 & 1u;
+        if (take & 8u) kept[i] = t + 3;
+        at += __popc(m0) + __popc(m1) + __popc(m2) + __popc(m3);
+    };
+    if (exact || same >= need || same + eq <= need) {  // the warp's ties go, or stay, together
+        const uint32_t least = !exact && same >= need ? bar + 1u : bar;
+        each([&](int t, const uint4 &k) {
+            put(t, (k.x >= least) | (k.y >= least) << 1 | (k.z >= least) << 2 | (k.w >= least) << 3);
+        });
+    } else {  // the row's last tie that stays is in this warp
+        each([&](int t, const uint4 &k) {
+            const unsigned tie = (k.x == bar) | (k.y == bar) << 1 | (k.z == bar) << 2 | (k.w == bar) << 3;
+            unsigned take = (k.x > bar) | (k.y > bar) << 1 | (k.z > bar) << 2 | (k.w > bar) << 3;
+            const unsigned n0 = __ballot_sync(0xffffffffu, tie & 1u), n1 = __ballot_sync(0xffffffffu, tie & 2u);
+            const unsigned n2 = __ballot_sync(0xffffffffu, tie & 4u), n3 = __ballot_sync(0xffffffffu, tie & 8u);
+            uint32_t r = same + __popc(n0 & below) + __popc(n1 & below) + __popc(n2 & below) + __popc(n3 & below);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (tie >> j & 1u) {
+                    if (r < (uint32_t)need) take |= 1u << j;
+                    ++r;
+                }
+            put(t, take);
+            same += __popc(n0) + __popc(n1) + __popc(n2) + __popc(n3);
+        });
+    }
+}
+
+// Launches `kernel` as launch_pdl does, in clusters of `cluster` CTAs.
+template <typename... KArgs, typename... Args>
+pkv_status launch_cluster(void (*kernel)(KArgs...), unsigned grid, unsigned block, unsigned cluster, size_t smem,
+                          cudaStream_t stream, Args &&...args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    PKV_CUDA_TRY(cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...));
+    return PKV_OK;
 }
 
 // ---- moves ---------------------------------------------------------------------
@@ -186,8 +361,17 @@ struct CompactParams {
     float *w;                    // accumulated weights, or NULL
     int64_t seq_stride, head_stride;
     int32_t chunk;               // rows per chunk (int8: whole blocks)
+    int32_t cluster;             // CTAs that share a unit of work
     int32_t *err;
 };
+
+// Every thread of the CTAs that share a unit has read its sources.
+__device__ __forceinline__ void unit_sync(int cluster) {
+    if (cluster > 1)
+        cg::this_cluster().sync();
+    else
+        __syncthreads();
+}
 
 // Where row i of (sequence, head) comes from and goes to: token rows of the
 // pool, or src < 0 for a row that is not moved because its data is bad.
@@ -225,7 +409,10 @@ __device__ __forceinline__ int64_t shfl64(int64_t x, int lane) {
     return (int64_t)__shfl_sync(0xffffffffu, (long long)x, lane);
 }
 
-// One CTA per (sequence, KV head, K or V).  RB: bytes of a head's row.
+// A cluster of p.cluster CTAs (1: no cluster) per (sequence, KV head, K or V),
+// its CTAs on neighbouring chunks.  A round loads one chunk per CTA, waits for
+// the cluster, and stores: the sources of a later round lie behind every row
+// that this one writes.  RB: bytes of a head's row.
 template <int RB>
 __global__ void __launch_bounds__(kMoveThreads) evict_compact_kernel(const CompactParams p) {
     constexpr int LPR = RB / 16;              // lanes per row
@@ -233,14 +420,15 @@ __global__ void __launch_bounds__(kMoveThreads) evict_compact_kernel(const Compa
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t unit = blockIdx.x;
+    const int64_t unit = blockIdx.x / p.cluster;
+    const int rank = (int)(blockIdx.x % p.cluster);
     const int which = (int)(unit & 1);
     const int64_t head = unit >> 1;           // (sequence, KV head)
     const int64_t seq = head / p.hkv;
     const int h = (int)(head - seq * p.hkv);
     const int L = p.seq_lens[seq];
     if (L < 0 || (int64_t)L > (int64_t)p.max_blocks * p.block_size) {
-        if (threadIdx.x == 0 && h == 0 && which == 0) set_err(p.err, PKV_DEVERR_LENGTH);
+        if (threadIdx.x == 0 && h == 0 && which == 0 && rank == 0) set_err(p.err, PKV_DEVERR_LENGTH);
         return;
     }
     if (L <= p.budget) return;                // every key stays where it is
@@ -250,7 +438,8 @@ __global__ void __launch_bounds__(kMoveThreads) evict_compact_kernel(const Compa
     uint8_t *pool = static_cast<uint8_t *>(which ? p.v : p.k) + (int64_t)h * RB;
     const int64_t pitch = (int64_t)p.hkv * RB;
     float *w = p.w && which == 0 ? p.w + seq * p.seq_stride + h * p.head_stride : nullptr;
-    for (int c0 = 0; c0 < n; c0 += kChunk) {
+    for (int base = 0; base < n; base += kChunk * p.cluster) {
+        const int c0 = base + rank * kChunk;
         const int i = c0 + warp * kMoveRows + lane;   // the row this lane looks up (lanes 0 .. 15)
         Move m;
         m.src = m.dst = -1;
@@ -265,7 +454,7 @@ __global__ void __launch_bounds__(kMoveThreads) evict_compact_kernel(const Compa
             const int64_t src = shfl64(m.src, u * (32 / LPR) + lane / LPR);
             if (src >= 0) r[u] = *(reinterpret_cast<const uint4 *>(pool + src * pitch) + lane % LPR);
         }
-        __syncthreads();  // every source of the chunk is read
+        unit_sync(p.cluster);  // every source of the round is read
 #pragma unroll
         for (int u = 0; u < LOADS; ++u) {
             const int from = u * (32 / LPR) + lane / LPR;
@@ -275,12 +464,59 @@ __global__ void __launch_bounds__(kMoveThreads) evict_compact_kernel(const Compa
         if (w && m.from > i) w[i] = wv;
     }
     if (w)
-        for (int t = n + threadIdx.x; t < L; t += kMoveThreads) w[t] = 0.f;
+        for (int t = n + rank * kMoveThreads + threadIdx.x; t < L; t += p.cluster * kMoveThreads) w[t] = 0.f;
 }
 
-__device__ __forceinline__ int32_t requantise(float x, float scale) {
+// Four codes as floats (the bytes, as code + 128, under the exponent of 2^23).
+__device__ __forceinline__ void code_floats(uint32_t word, float2 &lo, float2 &hi) {
+    const uint32_t x = word ^ 0x80808080u;
+    const float2 off = make_float2(-8388736.f, -8388736.f);
+    lo = __fadd2_rn(make_float2(__uint_as_float(__byte_perm(x, 0x4B000000u, 0x7540u)),
+                                __uint_as_float(__byte_perm(x, 0x4B000000u, 0x7541u))), off);
+    hi = __fadd2_rn(make_float2(__uint_as_float(__byte_perm(x, 0x4B000000u, 0x7542u)),
+                                __uint_as_float(__byte_perm(x, 0x4B000000u, 0x7543u))), off);
+}
+
+// The largest |code| of a word's even and odd bytes, joined to those in `m` (16-bit lanes).
+__device__ __forceinline__ uint32_t max_codes(uint32_t word, uint32_t m) {
+    const uint32_t s = (word >> 7) & 0x01010101u;
+    const uint32_t y = (word ^ (s * 255u)) + s;  // |code| <= 128 per byte: no carry
+    return __vmaxu2(__vmaxu2(m, y & 0x00FF00FFu), (y >> 8) & 0x00FF00FFu);
+}
+
+__device__ __forceinline__ uint32_t requantise_exact(float x, float scale) {
     const float r = rintf(__fdiv_rn(x, scale));
-    return (int32_t)fminf(fmaxf(r, -127.f), 127.f) & 255;
+    return (uint32_t)(int32_t)fminf(fmaxf(r, -127.f), 127.f) & 255u;
+}
+
+// Four codes with scale `from` under the scale `to` (> 0; inv = 1 / to): code' =
+// rint(fl(fl(code * from) / to)), at most 127.  The product with inv differs
+// from that quotient by less than 127 * 3 * 2^-24 < 2^-15, so unless it lies
+// within 2^-14 of a half it rounds to the same integer; adding 1.5 * 2^23
+// rounds it and leaves the integer in the low byte.  |code'| <= 127 holds but
+// for the last bits of |x| = the largest, 127 * to, which round to 127.
+__device__ __forceinline__ uint32_t requantise4(uint32_t word, float from, float to, float inv) {
+    const float2 magic = make_float2(12582912.f, 12582912.f), minus = make_float2(-12582912.f, -12582912.f);
+    float2 x[2];
+    code_floats(word, x[0], x[1]);
+    uint32_t out[2];
+    bool clear = true;
+    constexpr float kHalf = 0.5f - 6.1035156e-05f;  // 1/2 - 2^-14
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        x[i] = __fmul2_rn(x[i], make_float2(from, from));
+        const float2 q = __fmul2_rn(x[i], make_float2(inv, inv));
+        const float2 r = __fadd2_rn(q, magic);
+        const float2 t = __fadd2_rn(r, minus);
+        const float2 d = __fadd2_rn(q, make_float2(-t.x, -t.y));
+        clear = clear && fabsf(d.x) < kHalf && fabsf(d.y) < kHalf;
+        out[i] = __byte_perm(__float_as_uint(r.x), __float_as_uint(r.y), 0x0040u);
+    }
+    if (!clear) {  // near a half (or NaN: 1 / to overflowed): the division decides
+        return requantise_exact(x[0].x, to) | requantise_exact(x[0].y, to) << 8 | requantise_exact(x[1].x, to) << 16 |
+               requantise_exact(x[1].y, to) << 24;
+    }
+    return __byte_perm(out[0], out[1], 0x5410u);
 }
 
 // The int8 cache: a block in which some row of the head moves gets a new
@@ -294,14 +530,15 @@ __global__ void __launch_bounds__(kMoveThreads) evict_compact_i8_kernel(const Co
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t unit = blockIdx.x;
+    const int64_t unit = blockIdx.x / p.cluster;
+    const int rank = (int)(blockIdx.x % p.cluster);
     const int which = (int)(unit & 1);
     const int64_t head = unit >> 1;
     const int64_t seq = head / p.hkv;
     const int h = (int)(head - seq * p.hkv);
     const int L = p.seq_lens[seq];
     if (L < 0 || (int64_t)L > (int64_t)p.max_blocks * p.block_size) {
-        if (threadIdx.x == 0 && h == 0 && which == 0) set_err(p.err, PKV_DEVERR_LENGTH);
+        if (threadIdx.x == 0 && h == 0 && which == 0 && rank == 0) set_err(p.err, PKV_DEVERR_LENGTH);
         return;
     }
     if (L <= p.budget) return;
@@ -315,7 +552,8 @@ __global__ void __launch_bounds__(kMoveThreads) evict_compact_i8_kernel(const Co
     if (threadIdx.x < 3 * (kChunk / kMoveRows)) s_max[0][threadIdx.x] = 0u;
     __syncthreads();
     int round = 0;
-    for (int c0 = 0; c0 < n; c0 += p.chunk, round = round == 2 ? 0 : round + 1) {
+    for (int base = 0; base < n; base += p.chunk * p.cluster, round = round == 2 ? 0 : round + 1) {
+        const int c0 = base + rank * p.chunk;
         const int next = round == 2 ? 0 : round + 1;
         if (threadIdx.x < kChunk / kMoveRows) s_max[next][threadIdx.x] = 0u;
         const int local = warp * kMoveRows;             // first row of the warp in the chunk
@@ -343,41 +581,32 @@ __global__ void __launch_bounds__(kMoveThreads) evict_compact_i8_kernel(const Co
             rs[u] = __shfl_sync(0xffffffffu, sc, from);
             r[u] = make_uint4(0u, 0u, 0u, 0u);
             if (src >= 0) r[u] = *(reinterpret_cast<const uint4 *>(pool + src * pitch) + lane % LPR);
-            const uint32_t words[4] = {r[u].x, r[u].y, r[u].z, r[u].w};
-            int big = 0;
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-                for (int b = 0; b < 4; ++b) big = max(big, abs((int)(int8_t)(words[j] >> (8 * b))));
+            const uint32_t m = max_codes(r[u].w, max_codes(r[u].z, max_codes(r[u].y, max_codes(r[u].x, 0u))));
             // |code| * |scale| rounds monotonically in |code|: the row's largest value
-            top = fmaxf(top, __fmul_rn((float)big, fabsf(rs[u])));
+            top = fmaxf(top, __fmul_rn((float)max(m & 0xFFFFu, m >> 16), fabsf(rs[u])));
         }
         if (moved) {
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
             if (lane == 0) atomicMax(&s_max[round][slot], __float_as_uint(top));
         }
-        __syncthreads();  // every source of the chunk is read, every block's maximum known
+        unit_sync(p.cluster);  // every source of the round is read, every block's maximum known
         if (moved) {
             const float scale = __fdiv_rn(__uint_as_float(s_max[round][slot]), 127.f);
+            const float inv = __fdiv_rn(1.f, scale);
 #pragma unroll
             for (int u = 0; u < LOADS; ++u) {
                 const int from = u * (32 / LPR) + lane / LPR;
                 const int64_t dst = shfl64(m.dst, from);
-                uint32_t words[4] = {r[u].x, r[u].y, r[u].z, r[u].w};
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    uint32_t o = 0;
-#pragma unroll
-                    for (int b = 0; b < 4; ++b) {
-                        const float x = __fmul_rn((float)(int8_t)(words[j] >> (8 * b)), rs[u]);
-                        o |= (uint32_t)(scale > 0.f ? requantise(x, scale) : 0) << (8 * b);
-                    }
-                    words[j] = o;
+                if (scale > 0.f) {
+                    r[u].x = requantise4(r[u].x, rs[u], scale, inv);
+                    r[u].y = requantise4(r[u].y, rs[u], scale, inv);
+                    r[u].z = requantise4(r[u].z, rs[u], scale, inv);
+                    r[u].w = requantise4(r[u].w, rs[u], scale, inv);
+                } else {
+                    r[u] = make_uint4(0u, 0u, 0u, 0u);
                 }
-                if (dst >= 0)
-                    *(reinterpret_cast<uint4 *>(pool + dst * pitch) + lane % LPR) =
-                        make_uint4(words[0], words[1], words[2], words[3]);
+                if (dst >= 0) *(reinterpret_cast<uint4 *>(pool + dst * pitch) + lane % LPR) = r[u];
             }
             if (lane == 0 && local % p.block_size == 0 && m.dst >= 0)
                 scales[m.dst / p.block_size * p.hkv + h] = scale;
@@ -385,7 +614,7 @@ __global__ void __launch_bounds__(kMoveThreads) evict_compact_i8_kernel(const Co
         }
     }
     if (w)
-        for (int t = n + threadIdx.x; t < L; t += kMoveThreads) w[t] = 0.f;
+        for (int t = n + rank * kMoveThreads + threadIdx.x; t < L; t += p.cluster * kMoveThreads) w[t] = 0.f;
 }
 
 // Strides of the weights [num_seqs, num_kv_heads, max_keys], keys contiguous.
@@ -414,6 +643,26 @@ pkv_status check_compact(const int32_t *tables, int32_t max_blocks, const int32_
     return PKV_OK;
 }
 
+// CTAs per unit of work: enough for two to four CTAs on every SM, while a
+// round still has a chunk for each.
+pkv_status pick_cluster(CompactParams *p, int64_t units) {
+    int sms = 0;
+    pkv_status st = sm_count(-1, &sms);
+    if (st != PKV_OK) return st;
+    const int chunks = (p->budget + p->chunk - 1) / p->chunk;
+    p->cluster = 1;
+    while (p->cluster < 8 && units * p->cluster < 2 * sms && 2 * p->cluster <= chunks) p->cluster *= 2;
+    return PKV_OK;
+}
+
+pkv_status launch_compact(void (*kernel)(const CompactParams), CompactParams *p, int64_t units, cudaStream_t stream) {
+    pkv_status st = pick_cluster(p, units);
+    if (st != PKV_OK) return st;
+    const unsigned grid = (unsigned)(units * p->cluster);
+    if (p->cluster == 1) return launch_pdl(kernel, dim3(grid), dim3(kMoveThreads), 0, stream, *p);
+    return launch_cluster(kernel, grid, kMoveThreads, p->cluster, 0, stream, *p);
+}
+
 }  // namespace
 
 pkv_status check_cache_i8(const pkv_cache_i8 *c, const char *what);  // int8_write.cu
@@ -438,10 +687,41 @@ pkv_status pkv_evict_select(const float *weights, int64_t weights_seq_stride, in
     PKV_CHECK_ARG(new_lens != seq_lens, PKV_ERR_INVALID_ARG, "%s: new_lens must not be seq_lens", what);
     pkv_status st = check_weights(weights, weights_seq_stride, weights_head_stride, max_keys, num_kv_heads, what);
     if (st != PKV_OK) return st;
+    const int64_t rows = (int64_t)num_seqs * num_kv_heads;
     SelectParams p{weights, weights_seq_stride, weights_head_stride, seq_lens, num_kv_heads, max_keys, budget, sink,
-                   recent, kept, new_lens, err_word};
-    st = launch_pdl(evict_select_kernel, dim3((unsigned)((int64_t)num_seqs * num_kv_heads)), dim3(kSelThreads), 0, stream,
-                    p);
+                   recent, kept, new_lens, err_word, 1, 0};
+    // the rows' capacity (the lengths are on the device) picks the size: up to
+    // 4,096 keys to a CTA of four warps (2,048 rows of 512-4,096 keys, a CTA of
+    // 1, 2, 4, 8 warps per row: 35, 29, 27, 31 us), 16,384 to one of eight,
+    // 131,072 to a cluster of eight CTAs of 32; beyond that the keys do not stay
+    // on chip
+    constexpr int kSmem = 64 * 1024;
+    static std::atomic<uint64_t> smem_set[3];
+    if (max_keys <= 4096) {
+        p.run_chunks = (int)((max_keys + 511) / 512);
+        st = set_smem_once(reinterpret_cast<const void *>(evict_select_kernel<4, false, true>), kSmem, &smem_set[0]);
+        if (st != PKV_OK) return st;
+        st = launch_pdl(evict_select_kernel<4, false, true>, dim3((unsigned)rows), dim3(128),
+                        (size_t)p.run_chunks * 4 * 512, stream, p);
+    } else if (max_keys <= 16384) {
+        p.run_chunks = (int)((max_keys + 1023) / 1024);
+        st = set_smem_once(reinterpret_cast<const void *>(evict_select_kernel<8, false, true>), kSmem, &smem_set[1]);
+        if (st != PKV_OK) return st;
+        st = launch_pdl(evict_select_kernel<8, false, true>, dim3((unsigned)rows), dim3(256),
+                        (size_t)p.run_chunks * 8 * 512, stream, p);
+    } else {
+        const int64_t parts = (max_keys + 16383) / 16384;
+        p.cluster = parts <= 2 ? 2 : parts <= 4 ? 4 : kSelMaxCluster;
+        p.run_chunks = 4;
+        const unsigned grid = (unsigned)(rows * p.cluster);
+        if (parts <= kSelMaxCluster) {
+            st = set_smem_once(reinterpret_cast<const void *>(evict_select_kernel<32, true, true>), kSmem, &smem_set[2]);
+            if (st != PKV_OK) return st;
+            st = launch_cluster(evict_select_kernel<32, true, true>, grid, 1024, p.cluster, kSmem, stream, p);
+        } else {
+            st = launch_cluster(evict_select_kernel<32, true, false>, grid, 1024, p.cluster, 0, stream, p);
+        }
+    }
     return st == PKV_OK ? ok() : st;
 }
 
@@ -474,9 +754,8 @@ pkv_status pkv_evict_compact(const pkv_cache *cache, const int32_t *block_tables
     p.head_stride = weights_head_stride;
     p.chunk = kChunk;
     p.err = err_word;
-    const dim3 grid((unsigned)((int64_t)num_seqs * cache->num_kv_heads * 2));
-    st = cache->head_dim == 64 ? launch_pdl(evict_compact_kernel<128>, grid, dim3(kMoveThreads), 0, stream, p)
-                               : launch_pdl(evict_compact_kernel<256>, grid, dim3(kMoveThreads), 0, stream, p);
+    st = launch_compact(cache->head_dim == 64 ? evict_compact_kernel<128> : evict_compact_kernel<256>, &p,
+                        (int64_t)num_seqs * cache->num_kv_heads * 2, stream);
     return st == PKV_OK ? ok() : st;
 }
 
@@ -510,8 +789,7 @@ pkv_status pkv_evict_compact_int8(const pkv_cache_i8 *cache, const int32_t *bloc
     p.head_stride = weights_head_stride;
     p.chunk = kChunk / cache->block_size * cache->block_size;
     p.err = err_word;
-    const dim3 grid((unsigned)((int64_t)num_seqs * cache->num_kv_heads * 2));
-    st = launch_pdl(evict_compact_i8_kernel, grid, dim3(kMoveThreads), 0, stream, p);
+    st = launch_compact(evict_compact_i8_kernel, &p, (int64_t)num_seqs * cache->num_kv_heads * 2, stream);
     return st == PKV_OK ? ok() : st;
 }
 
