@@ -163,6 +163,17 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *r) {
         "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]));
 }
 
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+}
+
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]));
+}
+
 // max(a, b, c) in one instruction (three-input form of max.f32 on sm_100 and later)
 __device__ __forceinline__ float fmax3(float a, float b, float c) {
     float d;
@@ -215,6 +226,12 @@ __device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wa
 
 __device__ __forceinline__ void st_shared_u4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+__device__ __forceinline__ uint4 ld_shared_u4(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+    return v;
 }
 
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
@@ -274,6 +291,14 @@ template <int D>
 __host__ __device__ constexpr int prefill_stages() {  // stages of the K ring and of the V ring
     return D == 64 ? 4 : 2;
 }
+// int8: one K stage, refilled while the softmax of its step runs; the other's
+// place holds the codes in flight (16 bytes x 8 sub-blocks of K and of V per
+// converting thread)
+template <int D, bool I8>
+__host__ __device__ constexpr int prefill_k_stages() {
+    return I8 ? 1 : prefill_stages<D>();
+}
+constexpr int kCodeBytes = 2 * kTok * 128;
 
 // Registers per thread after the warpgroups re-balance them: the producer /
 // MMA warpgroup gives registers back, the two softmax warpgroups (a whole
@@ -285,15 +310,13 @@ __host__ __device__ constexpr int prefill_stages() {  // stages of the K ring an
 // and MMA warps spill 96 bytes and the softmax 28 more.  88 / 208 took the
 // mixed step's prefill chunks from 1,075 to 1,121 TFLOP/s (A/B on one box).
 //
-// int8 caches add a warpgroup that converts codes (512 threads, 128 registers
-// each at launch): 64 + 2 x 184 + 80 = 4 x 128.
+// int8 caches add a warpgroup that converts codes: 512 threads of 128
+// registers, enough for every role there, nothing re-balanced.
 template <bool I8>
 struct Regs {
     static constexpr int kThreads = I8 ? 512 : 384;
-    static constexpr int kLow = I8 ? 64 : 88;
-    static constexpr int kHigh = I8 ? 184 : 208;
-    static constexpr int kConv = 80;
-    static constexpr int kAtLaunchMin = (128 * (kLow + (I8 ? kConv : 0)) + 256 * kHigh + kThreads - 1) / kThreads;
+    static constexpr int kLow = 88, kHigh = 208;
+    static constexpr int kAtLaunchMin = I8 ? 0 : (128 * kLow + 256 * kHigh + kThreads - 1) / kThreads;
 };
 // Epilogue staging: each softmax warp passes 16 columns of its 32 O rows
 // through shared memory (row stride 20 floats: conflict-free 16-byte
@@ -301,6 +324,124 @@ struct Regs {
 // instruction instead of 32 rows x 16 bytes.
 constexpr int kStageStride = 20;
 constexpr int kStageBytes = 2 * 4 * 32 * kStageStride * 4;
+
+// Two values as bf16 pairs hi + lo: hi their upper halves (one byte permutation;
+// rounding costs a conversion and buys nothing), lo the rest, rounded: off by
+// at most 2^-16 of the value.
+__device__ __forceinline__ void split_bf16(float a, float b, uint32_t &hi, uint32_t &lo) {
+    hi = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632u);
+    const float2 rest = __fadd2_rn(make_float2(a, b), make_float2(-__uint_as_float(__float_as_uint(a) & 0xFFFF0000u),
+                                                                  -__uint_as_float(__float_as_uint(b) & 0xFFFF0000u)));
+    lo = pack2<__nv_bfloat16>(rest.x, rest.y);
+}
+
+// One step of a row's softmax over an int8 cache: 128 raw scores in TMEM become
+// P in their place (bf16, hi + lo).  Unlike the 16-bit step below, which holds
+// a whole row in registers, it walks 32 scores at a time with the next 32 in
+// flight, so that with a fourth warpgroup every thread fits the 128 registers
+// of a 512-thread launch (a whole row spilled 664 bytes and took 7,500 cycles a
+// step), and it is a loop of two parts per iteration: the softmax and the
+// converting warps run out of instruction cache when both are unrolled (mixed
+// step's chunks 703 -> 597 us).  `scl`: 8 factors of the scores (K scale,
+// softmax scale, log2 e), 8 V scales.  hi_c, lo_c: the row sees the step's keys
+// lo_c .. hi_c.
+// The running maximum moves when a score passes it by more than 15 (p <= 2^15):
+// then O, the sum and what the step has already written of P are scaled down.
+// (Letting the sum of 32 p tell instead, as the 16-bit step does, needs no
+// maximum but makes the next part wait for the vote: 460 -> 507 us.)
+template <int D>
+__device__ __forceinline__ void softmax_step_i8(uint32_t trow, const float *scl, bool whole, int hi_c, int lo_c,
+                                                bool has_o, float &m_used, float &lsum) {
+    constexpr float kLead = 15.f;
+    float2 sum = make_float2(0.f, 0.f);
+    uint32_t buf[2][32];
+    tmem_ld32(trow, buf[0]);
+#pragma unroll 1
+    for (int c2 = 0; c2 < kTok / 64; ++c2) {
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const int cc = 2 * c2 + half;
+            uint32_t(&sr)[32] = buf[half];
+            tmem_wait_ld();
+            if (cc + 1 < kTok / 32) tmem_ld32(trow + 32 * (cc + 1), buf[half ^ 1]);
+            const float2 ks = *reinterpret_cast<const float2 *>(scl + 2 * cc);
+            const float2 vs = *reinterpret_cast<const float2 *>(scl + 8 + 2 * cc);
+#pragma unroll
+            for (int c = 0; c < 32; c += 2) {
+                const float k = c < 16 ? ks.x : ks.y;
+                const float2 x =
+                    __fmul2_rn(make_float2(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), make_float2(k, k));
+                sr[c] = __float_as_uint(x.x);
+                sr[c + 1] = __float_as_uint(x.y);
+            }
+            if (!whole) {  // masked after the factor: a scale of 0 would turn a masked -inf into NaN
+#pragma unroll
+                for (int c = 0; c < 32; ++c)
+                    if (32 * cc + c > hi_c || 32 * cc + c < lo_c) sr[c] = __float_as_uint(-INFINITY);
+            }
+            float top[4];
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+                top[v] = fmax3(__uint_as_float(sr[8 * v]), __uint_as_float(sr[8 * v + 1]),
+                               fmax3(__uint_as_float(sr[8 * v + 2]), __uint_as_float(sr[8 * v + 3]),
+                                     fmax3(__uint_as_float(sr[8 * v + 4]), __uint_as_float(sr[8 * v + 5]),
+                                           fmaxf(__uint_as_float(sr[8 * v + 6]), __uint_as_float(sr[8 * v + 7])))));
+            const float most = fmaxf(fmax3(top[0], top[1], top[2]), top[3]);
+            const bool over = most > m_used + kLead || (m_used == -INFINITY && most > -INFINITY);
+            if (__any_sync(0xffffffffu, over)) {
+                const float m_new = over ? fmaxf(m_used, most) : m_used;
+                const float alpha = over ? fast_exp2(m_used - m_new) : 1.f;
+                m_used = m_new;
+                lsum *= alpha;
+                sum.x *= alpha;
+                sum.y *= alpha;
+                if (cc > 0) tmem_wait_st();  // the earlier parts of P have been written
+#pragma unroll 1
+                for (int i8 = 0; i8 < 2 * cc; ++i8) {  // 16 keys: eight columns of hi, eight of lo
+                    const uint32_t c0 = (uint32_t)(i8 >> 1) * 32u + (uint32_t)(i8 & 1) * 8u;
+                    uint32_t h[8], l[8];
+                    tmem_ld8(trow + c0, h);
+                    tmem_ld8(trow + c0 + 16, l);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float2 a = unpack2<__nv_bfloat16>(h[i]), b = unpack2<__nv_bfloat16>(l[i]);
+                        split_bf16((a.x + b.x) * alpha, (a.y + b.y) * alpha, h[i], l[i]);
+                    }
+                    tmem_st8(trow + c0, h);
+                    tmem_st8(trow + c0 + 16, l);
+                }
+                if (has_o) {
+#pragma unroll 1
+                    for (int c0 = 0; c0 < D; c0 += 8) {
+                        uint32_t o[8];
+                        tmem_ld8(trow + 128 + c0, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                        tmem_st8(trow + 128 + c0, o);
+                    }
+                }
+            }
+            // a row that has met no key yet: every score and m_used are -inf, p = 0
+            const float neg_m = m_used == -INFINITY ? -INFINITY : -m_used;
+            uint32_t ph[16], pl[16];
+#pragma unroll
+            for (int c = 0; c < 32; c += 2) {
+                const float v = c < 16 ? vs.x : vs.y;
+                const float2 x = __fadd2_rn(make_float2(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])),
+                                            make_float2(neg_m, neg_m));
+                const float2 pr = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+                sum = __fadd2_rn(sum, pr);
+                const float2 pv = __fmul2_rn(pr, make_float2(v, v));
+                split_bf16(pv.x, pv.y, ph[c / 2], pl[c / 2]);
+            }
+            tmem_st16(trow + 32 * cc, ph);
+            tmem_st16(trow + 32 * cc + 16, pl);
+        }
+    }
+    lsum += sum.x + sum.y;
+}
 
 // A work item: the pair of q tiles `pair` (2 x 128 M rows) of KV head `kvh`
 // of the prefill chunk of sequence `s`.  The producer warp finds a CTA's
@@ -314,8 +455,8 @@ struct TcItem {
 // products run on the codes, which are exact as 16-bit values: K in the query's
 // type, V in bf16.  Warps 12-15 read the codes through the block table,
 // convert them in registers and write the swizzled tiles that TMA writes
-// otherwise (8 loads in flight per thread, each register reloaded as soon as
-// its codes are converted), and leave the tile's 8 + 8 scales in a ring of
+// otherwise (asynchronous copies of the next step's codes into the thread's own
+// shared memory, refilled slot by slot), and leave the tile's 8 + 8 scales in a ring of
 // their own.  The softmax warps multiply the scores by their block's K scale
 // in binary32 and the weights by its V scale before they are split into a
 // bf16 hi + lo pair, whose exponent range holds any scale.
@@ -325,7 +466,8 @@ __global__ void __launch_bounds__(Regs<I8>::kThreads, 1)
                       const __grid_constant__ CUtensorMap tmv, const __grid_constant__ CUtensorMap tmo,
                       const TcParams p) {
     constexpr int HALVES = D / 64;
-    constexpr int S = prefill_stages<D>();
+    constexpr int S = prefill_stages<D>();           // V ring (and K ring of a 16-bit cache)
+    constexpr int SK = prefill_k_stages<D, I8>();    // K ring
     constexpr int QHALF = 128 * 128;            // bytes of 128 rows x 64 dims
     constexpr int QTILE = HALVES * QHALF;
     constexpr int KVHALF = kTok * 128;           // bytes of 128 tokens x 64 dims
@@ -345,14 +487,15 @@ __global__ void __launch_bounds__(Regs<I8>::kThreads, 1)
     __shared__ uint32_t s_tmem;
     __shared__ volatile int s_abort;
     // int8: scale * log2(e) * K scale and V scale of the 16-token sub-blocks of a
-    // step, slot = step % 4.  The fill of step g + 4 follows the release of K
-    // stage g + 2, whose score MMAs follow the softmax of step g + 1.
+    // step, slot = step % 4.  The fill of step g + 4 follows the release of step
+    // g + 3's K, whose score MMAs follow the softmax of step g + 2.
     __shared__ __align__(16) float s_scales[I8 ? 4 : 1][16];
     uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t *sq = base;
     uint8_t *sk = base + kTiles * QTILE;
-    uint8_t *sv = sk + S * KVSTAGE;
-    float *stage_o = reinterpret_cast<float *>(sv + S * KVSTAGE + 4096);
+    uint8_t *sv = sk + SK * KVSTAGE;
+    uint8_t *s_codes = sv + S * KVSTAGE;             // int8 only
+    float *stage_o = reinterpret_cast<float *>(s_codes + (I8 ? kCodeBytes : 0) + 4096);
     uint64_t *q_full = &bars[0];
     uint64_t *q_empty = &bars[1];  // every score MMA of an item has read its Q
     uint64_t *k_full = &bars[2];
@@ -412,7 +555,7 @@ __global__ void __launch_bounds__(Regs<I8>::kThreads, 1)
         return (kv_hi + kTok - 1) / kTok - it.j_first;
     };
     if (warp < 4) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<I8>::kLow));
+        if constexpr (!I8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<I8>::kLow));
     if (warp == 0) {
         // ===== producer: finds the items, then Q of both tiles and the K and V tiles of each =====
         const uint64_t pol_q = policy_evict_first();
@@ -601,7 +744,7 @@ __global__ void __launch_bounds__(Regs<I8>::kThreads, 1)
         const uint32_t sq_a = smem_u32(sq), sk_a = smem_u32(sk), sv_a = smem_u32(sv);
         // g: ring position of the K / V step
         auto issue_s = [&](int u, int g) {
-            const uint32_t kst = sk_a + (g % S) * KVSTAGE;
+            const uint32_t kst = sk_a + (g % SK) * KVSTAGE;
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
                 const int half = kk >> 2, koff = (kk & 3) * 32;
@@ -638,7 +781,7 @@ __global__ void __launch_bounds__(Regs<I8>::kThreads, 1)
             // V rows past kv_len (only in the last step) are cleared by the first
             // tile whose P V reads that step
             const int zt = nt0 == nt ? 0 : 1;
-            ok = wait(q_full, it & 1) && wait(&k_full[gc % S], (gc / S) & 1);
+            ok = wait(q_full, it & 1) && wait(&k_full[gc % SK], (gc / SK) & 1);
             if (!ok) break;
             tc_fence_after();
 #pragma unroll
@@ -653,7 +796,7 @@ __global__ void __launch_bounds__(Regs<I8>::kThreads, 1)
                 issue_s(u, gc);
             }
             if (!ok) break;
-            umma_commit(&k_empty[gc % S]);
+            umma_commit(&k_empty[gc % SK]);
             if (nt == 1) umma_commit(q_empty);  // every score MMA of the item issued
             for (int j = 0; j < nt && ok; ++j) {
                 const int g = gc + j;
@@ -679,7 +822,7 @@ __global__ void __launch_bounds__(Regs<I8>::kThreads, 1)
                     // here, in the shadow of the next wait
                     if (u == kTiles - 1 || j >= nt1) umma_commit(&v_empty[g % S]);
                     if (j1 < steps_of(u)) {
-                        if (!k_ready) ok = k_ready = wait(&k_full[(g + 1) % S], ((g + 1) / S) & 1);
+                        if (!k_ready) ok = k_ready = wait(&k_full[(g + 1) % SK], ((g + 1) / SK) & 1);
                         // the scores overwrite P of step j: its P V must have completed
                         if (ok) ok = wait(o_done(u), ph);
                         if (!ok) continue;
@@ -688,7 +831,7 @@ __global__ void __launch_bounds__(Regs<I8>::kThreads, 1)
                     }
                 }
                 if (!ok) break;
-                if (k_ready) umma_commit(&k_empty[(g + 1) % S]);
+                if (k_ready) umma_commit(&k_empty[(g + 1) % SK]);
                 if (j1 == nt - 1) umma_commit(q_empty);  // every score MMA of the item issued
             }
             tb[0] += nt0;
@@ -701,13 +844,13 @@ __global__ void __launch_bounds__(Regs<I8>::kThreads, 1)
         }
     }
     } else if (I8 && warp >= 12) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<I8>::kConv));
         // ===== int8: codes to 16-bit tiles =====
         // thread = 16 codes (col) of row r16 of every 16-token sub-block of a tile
         const int col = tid & 7, r16 = (tid & 127) >> 3;
         const int64_t pitch = (int64_t)p.hkv * D;
         const uint32_t sk_a = smem_u32(sk), sv_a = smem_u32(sv);
-        constexpr int SUBS = kTok / 16;
+        constexpr int SUBS = kTok / 16, CONV = 2;  // sub-blocks of a tile; converted at a time
+        const uint32_t k_slot = smem_u32(s_codes) + (tid & 127) * 16, v_slot = k_slot + kCodeBytes / 2;
         int gs = 0;  // ring position
         bool ok = true;
         for (int it = 0; ok; ++it) {
@@ -737,57 +880,82 @@ __global__ void __launch_bounds__(Regs<I8>::kThreads, 1)
                 }
                 row = phys * p.block_size + (tok - lb * p.block_size);
             };
-            uint4 r[SUBS];
-            auto load = [&](const int8_t *pool, int i) {
+            // this thread's codes of sub-block i, K or V, of the next step: into its own 16 bytes
+            auto fetch = [&](const int8_t *pool, uint32_t slot, int i) {
                 const int rr = __shfl_sync(0xffffffffu, row, i);
-                r[i] = rr >= 0 ? __ldg(reinterpret_cast<const uint4 *>(pool + rr * pitch + off)) : make_uint4(0u, 0u, 0u, 0u);
+                const int8_t *src = pool + (rr >= 0 ? rr * pitch + off : 0);
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(slot + i * 2048), "l"(src),
+                             "r"(rr >= 0 ? 16 : 0)
+                             : "memory");
             };
-            lookup(0);
-#pragma unroll
-            for (int i = 0; i < SUBS; ++i) load(p.kq, i);
-            for (int j = 0; j < nt; ++j, ++gs) {
-                const int stage = gs % S;
-                const uint32_t free_parity = ((gs / S) & 1) ^ 1;
-                float ks = 0.f, vs = 0.f;
-                if (warp == 12 && lane < SUBS && phys >= 0) {
+            float ks = 0.f, vs = 0.f;  // warp 12, lane i < 8: the factors of sub-block i of the next step
+            auto load_scales = [&] {
+                ks = vs = 0.f;
+                if (warp == 12 && phys >= 0) {
                     ks = p.k_scale[(int64_t)phys * p.hkv + item.kvh] * p.scale_log2;
                     vs = p.v_scale[(int64_t)phys * p.hkv + item.kvh];
                 }
-                ok = __all_sync(0xffffffffu, wait_phase(&k_empty[stage], free_parity, &s_abort));
+            };
+            lookup(0);
+            load_scales();
+            for (int i = 0; i < SUBS; ++i) fetch(p.kq, k_slot, i);
+            asm volatile("cp.async.commit_group;" ::: "memory");
+            for (int i = 0; i < SUBS; ++i) fetch(p.vq, v_slot, i);
+            asm volatile("cp.async.commit_group;" ::: "memory");
+            for (int j = 0; j < nt; ++j, ++gs) {
+                ok = __all_sync(0xffffffffu, wait_phase(&k_empty[gs % SK], ((gs / SK) & 1) ^ 1, &s_abort));
                 if (!ok) break;
                 if (warp == 12 && lane < SUBS) {
                     s_scales[I8 ? gs & 3 : 0][lane] = ks;
                     s_scales[I8 ? gs & 3 : 0][8 + lane] = vs;
                 }
-#pragma unroll
-                for (int i = 0; i < SUBS; ++i) {
-                    const uint4 v = r[i];
-                    load(p.vq, i);
-                    store_codes<T>(sk_a + stage * KVSTAGE, KVHALF, i * 16 + r16, col, v);
-                }
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&k_full[stage]);
                 lookup(j + 1);
-                ok = __all_sync(0xffffffffu, wait_phase(&v_empty[stage], free_parity, &s_abort));
-                if (!ok) break;
+                load_scales();
+                // not unrolled, here and below: four warps on code of their own beside the
+                // softmax's would run out of instruction cache
+                asm volatile("cp.async.wait_group 1;" ::: "memory");
+#pragma unroll 1
+                for (int i = 0; i < SUBS; i += CONV) {
+                    uint4 v[CONV];
 #pragma unroll
-                for (int i = 0; i < SUBS; ++i) {
-                    const uint4 v = r[i];
-                    load(p.kq, i);
-                    store_codes<TP>(sv_a + stage * KVSTAGE, KVHALF, i * 16 + r16, col, v);
+                    for (int e = 0; e < CONV; ++e) v[e] = ld_shared_u4(k_slot + (i + e) * 2048);
+#pragma unroll
+                    for (int e = 0; e < CONV; ++e)
+                        store_codes<T>(sk_a + (gs % SK) * KVSTAGE, KVHALF, (i + e) * 16 + r16, col, v[e]);
+#pragma unroll
+                    for (int e = 0; e < CONV; ++e) fetch(p.kq, k_slot, i + e);
                 }
+                asm volatile("cp.async.commit_group;" ::: "memory");
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&v_full[stage]);
+                if (lane == 0) mbar_arrive(&k_full[gs % SK]);
+                ok = __all_sync(0xffffffffu, wait_phase(&v_empty[gs % S], ((gs / S) & 1) ^ 1, &s_abort));
+                if (!ok) break;
+                asm volatile("cp.async.wait_group 1;" ::: "memory");
+#pragma unroll 1
+                for (int i = 0; i < SUBS; i += CONV) {
+                    uint4 v[CONV];
+#pragma unroll
+                    for (int e = 0; e < CONV; ++e) v[e] = ld_shared_u4(v_slot + (i + e) * 2048);
+#pragma unroll
+                    for (int e = 0; e < CONV; ++e)
+                        store_codes<TP>(sv_a + (gs % S) * KVSTAGE, KVHALF, (i + e) * 16 + r16, col, v[e]);
+#pragma unroll
+                    for (int e = 0; e < CONV; ++e) fetch(p.vq, v_slot, i + e);
+                }
+                asm volatile("cp.async.commit_group;" ::: "memory");
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&v_full[gs % S]);
             }
+            asm volatile("cp.async.wait_all;" ::: "memory");  // (nothing but zeros is in flight behind the last step)
         }
         if (!ok && lane == 0) {
             s_abort = 1;
             set_err(p.err, PKV_DEVERR_TIMEOUT);
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Regs<I8>::kHigh));
+        if constexpr (!I8) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Regs<I8>::kHigh));
         // ===== softmax + epilogue: warps 4-7 tile 0, warps 8-11 tile 1, one M row per thread =====
         const int u = (warp - 4) >> 2;
         const int qw = warp & 3;  // a warp reaches TMEM lanes 32 * (warp % 4) .. + 31
@@ -839,160 +1007,133 @@ __global__ void __launch_bounds__(Regs<I8>::kThreads, 1)
                 const int t0 = (j_first + j) * kTok;
                 // every row of the warp sees every key of the tile: no masking
                 const bool whole = __all_sync(0xffffffffu, t0 + kTok - 1 <= lim && t0 >= lo);
-                // the row's 128 scores, read with one wait (each wait exposes the
-                // whole TMEM load latency)
-                uint32_t sr[kTok];
-#pragma unroll
-                for (int c0 = 0; c0 < kTok; c0 += 32)
-                    tmem_ld32(trow_addr + c0, *reinterpret_cast<uint32_t(*)[32]>(&sr[c0]));
-                tmem_wait_ld();
-                // int8: a masked step's scores take their K scale here (a scale of 0
-                // would turn a masked -inf into NaN), a whole step's below
-                const float *scl = s_scales[I8 ? gpos & 3 : 0];
                 if constexpr (I8) {
-                    if (!whole) {
-#pragma unroll
-                        for (int c = 0; c < kTok; ++c) sr[c] = __float_as_uint(__uint_as_float(sr[c]) * scl[c / 16]);
-                    }
-                }
-                auto k_mul = [&](int c) -> float { return whole ? scl[c / 16] : 1.f; };
-                if (!whole) {
-                    // keys t0 + c with c > lim - t0 (causal limit) or c < lo - t0
-                    // (window start) are invisible; the start only matters on
-                    // steps that begin before it
-                    const int hi_c = lim - t0, lo_c = lo - t0;
-#pragma unroll
-                    for (int c = 0; c < kTok; ++c)
-                        if (c > hi_c) sr[c] = __float_as_uint(-INFINITY);
-                    if (__any_sync(0xffffffffu, lo_c > 0)) {
-#pragma unroll
-                        for (int c = 0; c < kTok; ++c)
-                            if (c < lo_c) sr[c] = __float_as_uint(-INFINITY);
-                    }
-                }
-                // the row max of the raw scores times the scale (positive): eight
-                // independent chains of three-input maxima
-                auto row_max = [&]() -> float {
-                    float pm[8];
-                    if constexpr (I8) {  // taken on few steps: the products one by one
-                        pm[0] = -INFINITY;
+                    softmax_step_i8<D>(trow_addr, s_scales[I8 ? gpos & 3 : 0], whole, lim - t0, lo - t0, j > 0, m_used,
+                                       lsum);
+                } else {
+                    // the row's 128 scores, read with one wait (each wait exposes the
+                    // whole TMEM load latency)
+                    uint32_t sr[kTok];
     #pragma unroll
-                        for (int c = 0; c < kTok; ++c) pm[0] = fmaxf(pm[0], __uint_as_float(sr[c]) * k_mul(c));
-                        return pm[0];
-                    } else {
-        #pragma unroll
+                    for (int c0 = 0; c0 < kTok; c0 += 32)
+                        tmem_ld32(trow_addr + c0, *reinterpret_cast<uint32_t(*)[32]>(&sr[c0]));
+                    tmem_wait_ld();
+                    if (!whole) {
+                        // keys t0 + c with c > lim - t0 (causal limit) or c < lo - t0
+                        // (window start) are invisible; the start only matters on
+                        // steps that begin before it
+                        const int hi_c = lim - t0, lo_c = lo - t0;
+    #pragma unroll
+                        for (int c = 0; c < kTok; ++c)
+                            if (c > hi_c) sr[c] = __float_as_uint(-INFINITY);
+                        if (__any_sync(0xffffffffu, lo_c > 0)) {
+    #pragma unroll
+                            for (int c = 0; c < kTok; ++c)
+                                if (c < lo_c) sr[c] = __float_as_uint(-INFINITY);
+                        }
+                    }
+                    // the row max of the raw scores times the scale (positive): eight
+                    // independent chains of three-input maxima
+                    auto row_max = [&]() -> float {
+                        float pm[8];
+#pragma unroll
                         for (int v = 0; v < 8; ++v) pm[v] = fmaxf(__uint_as_float(sr[v]), __uint_as_float(sr[8 + v]));
-        #pragma unroll
+#pragma unroll
                         for (int c = 16; c < kTok; c += 16)
-        #pragma unroll
+#pragma unroll
                             for (int v = 0; v < 8; ++v)
                                 pm[v] = fmax3(pm[v], __uint_as_float(sr[c + v]), __uint_as_float(sr[c + 8 + v]));
                         return fmaxf(fmax3(pm[0], pm[1], pm[2]), fmax3(pm[3], pm[4], fmax3(pm[5], pm[6], pm[7]))) * sl;
-                    }
-                };
-                // The running max m_used is taken from the row's first tile with
-                // a visible key and is moved only when p would leave the range
-                // where it is exact enough and finite as a 16-bit value: every p of
-                // a step is at most the step's sum, so a sum <= 2^15 proves all p
-                // <= 2^15.  Otherwise (or on inf / NaN) the row takes the exact
-                // max, O and the row sum are rescaled, and P is written again (a
-                // second pass of the loop below).
-                const bool fresh = m_used == -INFINITY;
-                if (__any_sync(0xffffffffu, fresh) && fresh) m_used = row_max();
-                float step_sum;
-    #pragma unroll 1
-                for (int pass = 0;; ++pass) {
-                    // p = 2^(s * scale - m_used), written back over the scores as
-                    // 16-bit values (the scale and shift, and the row sum, as packed
-                    // fp32 pairs).  While a row has met no key yet (a window can
-                    // start past whole tiles) every score and m_used are -inf: the
-                    // shift is then taken as -inf too, so every p is 0, not NaN.
-                    const float neg_m = m_used == -INFINITY ? -INFINITY : -m_used;
-                    const float2 sl2 = make_float2(sl, sl), nm2 = make_float2(neg_m, neg_m);
-                    float2 ps[4];
-    #pragma unroll
-                    for (int v = 0; v < 4; ++v) ps[v] = make_float2(0.f, 0.f);
-    #pragma unroll
-                    for (int c0 = 0; c0 < kTok; c0 += 32) {
-                        uint32_t ph[16], pl[16];
-                        float2 kv2[2][2];  // int8: (K factor, V scale) of the chunk's two sub-blocks
-                        if constexpr (I8) {
-    #pragma unroll
-                            for (int b = 0; b < 2; ++b) {
-                                const float kf = k_mul(c0 + 16 * b), vf = scl[8 + c0 / 16 + b];
-                                kv2[b][0] = make_float2(kf, kf);
-                                kv2[b][1] = make_float2(vf, vf);
+                    };
+                    // The running max m_used is taken from the row's first tile with
+                    // a visible key and is moved only when p would leave the range
+                    // where it is exact enough and finite as a 16-bit value: every p of
+                    // a step is at most the step's sum, so a sum <= 2^15 proves all p
+                    // <= 2^15.  Otherwise (or on inf / NaN) the row takes the exact
+                    // max, O and the row sum are rescaled, and P is written again (a
+                    // second pass of the loop below).
+                    const bool fresh = m_used == -INFINITY;
+                    if (__any_sync(0xffffffffu, fresh) && fresh) m_used = row_max();
+                    float step_sum;
+#pragma unroll 1
+                    for (int pass = 0;; ++pass) {
+                        // p = 2^(s * scale - m_used), written back over the scores as
+                        // 16-bit values (the scale and shift, and the row sum, as packed
+                        // fp32 pairs).  While a row has met no key yet (a window can
+                        // start past whole tiles) every score and m_used are -inf: the
+                        // shift is then taken as -inf too, so every p is 0, not NaN.
+                        const float neg_m = m_used == -INFINITY ? -INFINITY : -m_used;
+                        const float2 sl2 = make_float2(sl, sl), nm2 = make_float2(neg_m, neg_m);
+                        float2 ps[4];
+#pragma unroll
+                        for (int v = 0; v < 4; ++v) ps[v] = make_float2(0.f, 0.f);
+#pragma unroll
+                        for (int c0 = 0; c0 < kTok; c0 += 32) {
+                            uint32_t ph[16], pl[16];
+#pragma unroll
+                            for (int c = 0; c < 32; c += 2) {
+                                const float2 x = __ffma2_rn(
+                                    make_float2(__uint_as_float(sr[c0 + c]), __uint_as_float(sr[c0 + c + 1])), sl2, nm2);
+                                const float p0 = fast_exp2(x.x), p1 = fast_exp2(x.y);
+                                ps[(c >> 1) & 3] = __fadd2_rn(ps[(c >> 1) & 3], make_float2(p0, p1));
+                                const uint32_t h = pack2<T>(p0, p1);
+                                ph[c / 2] = h;
+                                if (LO) {
+                                    const float2 hf = unpack2<T>(h);
+                                    pl[c / 2] = pack2<T>(p0 - hf.x, p1 - hf.y);
+                                }
                             }
-                        }
-    #pragma unroll
-                        for (int c = 0; c < 32; c += 2) {
-                            const float2 x = __ffma2_rn(
-                                make_float2(__uint_as_float(sr[c0 + c]), __uint_as_float(sr[c0 + c + 1])),
-                                I8 ? kv2[c / 16][0] : sl2, nm2);
-                            float p0 = fast_exp2(x.x), p1 = fast_exp2(x.y);
-                            ps[(c >> 1) & 3] = __fadd2_rn(ps[(c >> 1) & 3], make_float2(p0, p1));
-                            if constexpr (I8) {
-                                const float2 pv = __fmul2_rn(make_float2(p0, p1), kv2[c / 16][1]);
-                                p0 = pv.x;
-                                p1 = pv.y;
-                            }
-                            const uint32_t h = pack2<TP>(p0, p1);
-                            ph[c / 2] = h;
                             if (LO) {
-                                const float2 hf = unpack2<TP>(h);
-                                pl[c / 2] = pack2<TP>(p0 - hf.x, p1 - hf.y);
+                                tmem_st16(trow_addr + c0, ph);
+                                tmem_st16(trow_addr + c0 + 16, pl);
+                            } else {
+                                tmem_st16(trow_addr + c0 / 2, ph);
                             }
                         }
-                        if (LO) {
-                            tmem_st16(trow_addr + c0, ph);
-                            tmem_st16(trow_addr + c0 + 16, pl);
-                        } else {
-                            tmem_st16(trow_addr + c0 / 2, ph);
+                        const float2 ps01 = __fadd2_rn(ps[0], ps[1]), ps23 = __fadd2_rn(ps[2], ps[3]);
+                        const float2 ps4 = __fadd2_rn(ps01, ps23);
+                        step_sum = ps4.x + ps4.y;
+                        const bool over = pass == 0 && !(step_sum <= kPSumMax);
+                        if (!__any_sync(0xffffffffu, over)) break;
+                        tmem_wait_st();
+                        float alpha = 1.f;
+                        if (over) {
+                            const float m_new = fmaxf(m_used, row_max());
+                            alpha = fast_exp2(m_used - m_new);
+                            lsum *= alpha;
+                            m_used = m_new;
+                        }
+                        if (j > 0) {
+#pragma unroll
+                            for (int c0 = 0; c0 < D; c0 += 32) {
+                                uint32_t orr[32];
+                                tmem_ld32(trow_addr + 128 + c0, orr);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int c = 0; c < 32; ++c) orr[c] = __float_as_uint(__uint_as_float(orr[c]) * alpha);
+                                tmem_st32(trow_addr + 128 + c0, orr);
+                            }
                         }
                     }
-                    const float2 ps01 = __fadd2_rn(ps[0], ps[1]), ps23 = __fadd2_rn(ps[2], ps[3]);
-                    const float2 ps4 = __fadd2_rn(ps01, ps23);
-                    step_sum = ps4.x + ps4.y;
-                    const bool over = pass == 0 && !(step_sum <= kPSumMax);
-                    if (!__any_sync(0xffffffffu, over)) break;
-                    tmem_wait_st();
-                    float alpha = 1.f;
-                    if (over) {
-                        const float m_new = fmaxf(m_used, row_max());
-                        alpha = fast_exp2(m_used - m_new);
-                        lsum *= alpha;
-                        m_used = m_new;
-                    }
-                    if (j > 0) {
-    #pragma unroll
-                        for (int c0 = 0; c0 < D; c0 += 32) {
-                            uint32_t orr[32];
-                            tmem_ld32(trow_addr + 128 + c0, orr);
-                            tmem_wait_ld();
-    #pragma unroll
-                            for (int c = 0; c < 32; ++c) orr[c] = __float_as_uint(__uint_as_float(orr[c]) * alpha);
-                            tmem_st32(trow_addr + 128 + c0, orr);
+                    lsum += step_sum;
+                    // V rows past kv_len in the last tile hold stale or unrelated data:
+                    // zero them, once the tile's TMA load (which may cover some of
+                    // them) has landed
+                    if (j == jzero) {
+                        if (!wait_phase(&v_full[gpos % S], (gpos / S) & 1, &s_abort)) {
+                            s_abort = 1;
+                            set_err(p.err, PKV_DEVERR_TIMEOUT);
                         }
-                    }
-                }
-                lsum += step_sum;
-                // V rows past kv_len in the last tile hold stale or unrelated data:
-                // zero them, once the tile's TMA load (which may cover some of
-                // them) has landed
-                if (j == jzero) {
-                    if (!wait_phase(&v_full[gpos % S], (gpos / S) & 1, &s_abort)) {
-                        s_abort = 1;
-                        set_err(p.err, PKV_DEVERR_TIMEOUT);
-                    }
-                    if (row >= item.kv_len - t0) {
-    #pragma unroll
-                        for (int half = 0; half < HALVES; ++half) {
-                            uint4 *dst = reinterpret_cast<uint4 *>(sv + (gpos % S) * KVSTAGE + half * KVHALF + row * 128);
-    #pragma unroll
-                            for (int c = 0; c < 8; ++c) dst[c] = make_uint4(0u, 0u, 0u, 0u);
+                        if (row >= item.kv_len - t0) {
+#pragma unroll
+                            for (int half = 0; half < HALVES; ++half) {
+                                uint4 *dst = reinterpret_cast<uint4 *>(sv + (gpos % S) * KVSTAGE + half * KVHALF + row * 128);
+#pragma unroll
+                                for (int c = 0; c < 8; ++c) dst[c] = make_uint4(0u, 0u, 0u, 0u);
+                            }
                         }
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     }
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 }
                 tmem_wait_st();
                 tc_fence_before();
@@ -1153,8 +1294,9 @@ static pkv_status launch_prefill_tc_t(const CUtensorMap &mq, const CUtensorMap &
     // Q of both tiles + the K and V rings, + 1 KB for the 1024-byte alignment
     // of the swizzled tiles, + 4 KB of slack after the last stage, + the
     // epilogue staging rows
-    const int smem = kTiles * HALVES * 128 * 128 + 2 * prefill_stages<D>() * HALVES * kTok * 128 + 1024 + 4096 +
-                     kStageBytes;
+    const int smem = kTiles * HALVES * 128 * 128 +
+                     (prefill_stages<D>() + prefill_k_stages<D, I8>()) * HALVES * kTok * 128 + (I8 ? kCodeBytes : 0) + 1024 +
+                     4096 + kStageBytes;
     auto kern = prefill_tc_kernel<D, T, I8>;
     static std::atomic<uint64_t> smem_set{0};
     pkv_status st = set_smem_once(reinterpret_cast<const void *>(kern), smem, &smem_set);
