@@ -118,14 +118,15 @@ pkv_status encode_pool_rows_map(CUtensorMap *map, void *base, const pkv_cache *c
 }
 
 // The int8 pool the same way: chunks are whole KV heads (128 codes).
-pkv_status encode_pool_rows_map_i8(CUtensorMap *map, void *base, const pkv_cache_i8 *c, int heads) {
+pkv_status encode_pool_rows_map_i8(CUtensorMap *map, void *base, const pkv_cache_i8 *c, int heads, int rows) {
     auto fn = encode_fn();
     PKV_CHECK_ARG(fn, PKV_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
-    PKV_CHECK_ARG(heads >= 1 && heads <= c->num_kv_heads, PKV_ERR_INVALID_ARG, "int8 pool box of %d heads", heads);
+    PKV_CHECK_ARG(heads >= 1 && heads <= c->num_kv_heads && heads <= 256 && rows >= 1 && rows <= 256, PKV_ERR_INVALID_ARG,
+                  "int8 pool box of %d rows, %d heads", rows, heads);
     cuuint64_t dims[3] = {(cuuint64_t)c->head_dim, (cuuint64_t)c->num_blocks * c->block_size,
                           (cuuint64_t)c->num_kv_heads};
     cuuint64_t strides[2] = {(cuuint64_t)c->num_kv_heads * c->head_dim, (cuuint64_t)c->head_dim};
-    cuuint32_t box[3] = {128, 16, (cuuint32_t)heads};
+    cuuint32_t box[3] = {128, (cuuint32_t)rows, (cuuint32_t)heads};
     cuuint32_t estr[3] = {1, 1, 1};
     CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);

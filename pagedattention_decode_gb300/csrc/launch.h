@@ -69,7 +69,7 @@ pkv_status encode_pool_rows_map(CUtensorMap *map, void *base, const pkv_cache *c
 // [heads][rows][D] view of packed output rows: one box = 64 bytes x rows x heads
 pkv_status encode_out_map(CUtensorMap *map, void *out, int total_q, int hq, int d, int out_dtype, int cols, int rows,
                           int heads);
-pkv_status encode_pool_rows_map_i8(CUtensorMap *map, void *base, const pkv_cache_i8 *c, int heads);
+pkv_status encode_pool_rows_map_i8(CUtensorMap *map, void *base, const pkv_cache_i8 *c, int heads, int rows = 16);
 
 // 3-D tensor map over packed query rows [total_q][Hq * D / 64][64] (row
 // stride q_stride elements), box = `rows` rows x 1 x 64 elements, 128-byte

@@ -85,8 +85,7 @@ struct TcParams {
     int32_t box_rows; // rows per K/V TMA box: 128, 64, 32 or 16, a divisor of block_size
     int32_t num_seqs;
     int32_t out_tma;  // the output map is valid: whole warps' rows leave by TMA stores
-    const int8_t *kq, *vq;  // int8 cache: code pools [num_blocks * block_size, hkv, D], scales [num_blocks, hkv]
-    const float *k_scale, *v_scale;
+    const float *k_scale, *v_scale;  // int8 cache: [num_blocks, hkv]
 };
 
 // UMMA shared-memory descriptor, 128-byte swizzle (sm_100 family layout:
@@ -292,8 +291,7 @@ __host__ __device__ constexpr int prefill_stages() {  // stages of the K ring an
     return D == 64 ? 4 : 2;
 }
 // int8: one K stage, refilled while the softmax of its step runs; the other's
-// place holds the codes in flight (16 bytes x 8 sub-blocks of K and of V per
-// converting thread)
+// place holds the staged codes of a step
 template <int D, bool I8>
 __host__ __device__ constexpr int prefill_k_stages() {
     return I8 ? 1 : prefill_stages<D>();
@@ -337,108 +335,102 @@ __device__ __forceinline__ void split_bf16(float a, float b, uint32_t &hi, uint3
 
 // One step of a row's softmax over an int8 cache: 128 raw scores in TMEM become
 // P in their place (bf16, hi + lo).  Unlike the 16-bit step below, which holds
-// a whole row in registers, it walks 32 scores at a time with the next 32 in
-// flight, so that with a fourth warpgroup every thread fits the 128 registers
-// of a 512-thread launch (a whole row spilled 664 bytes and took 7,500 cycles a
-// step), and it is a loop of two parts per iteration: the softmax and the
-// converting warps run out of instruction cache when both are unrolled (mixed
-// step's chunks 703 -> 597 us).  `scl`: 8 factors of the scores (K scale,
+// a whole row in registers, it walks 32 scores at a time, so that with a fourth
+// warpgroup every thread fits the 128 registers of a 512-thread launch (a whole
+// row spilled 664 bytes), and in a loop that is not unrolled: beside the
+// converting warps' code the instruction cache is what runs out (chunks of the
+// mixed step, 16 x 512 rows over 2,560 keys, us: four parts unrolled 519, two 421,
+// one 404, though its TMEM loads are not overlapped).  `scl`: 8 factors of the scores (K scale,
 // softmax scale, log2 e), 8 V scales.  hi_c, lo_c: the row sees the step's keys
 // lo_c .. hi_c.
 // The running maximum moves when a score passes it by more than 15 (p <= 2^15):
 // then O, the sum and what the step has already written of P are scaled down.
 // (Letting the sum of 32 p tell instead, as the 16-bit step does, needs no
-// maximum but makes the next part wait for the vote: 460 -> 507 us.)
+// maximum but makes the next part wait for the vote: 460 -> 507 us then.)
 template <int D>
 __device__ __forceinline__ void softmax_step_i8(uint32_t trow, const float *scl, bool whole, int hi_c, int lo_c,
                                                 bool has_o, float &m_used, float &lsum) {
     constexpr float kLead = 15.f;
     float2 sum = make_float2(0.f, 0.f);
-    uint32_t buf[2][32];
-    tmem_ld32(trow, buf[0]);
 #pragma unroll 1
-    for (int c2 = 0; c2 < kTok / 64; ++c2) {
+    for (int cc = 0; cc < kTok / 32; ++cc) {
+        uint32_t sr[32];
+        tmem_ld32(trow + 32 * cc, sr);
+        tmem_wait_ld();
+        const float2 ks = *reinterpret_cast<const float2 *>(scl + 2 * cc);
+        const float2 vs = *reinterpret_cast<const float2 *>(scl + 8 + 2 * cc);
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            const int cc = 2 * c2 + half;
-            uint32_t(&sr)[32] = buf[half];
-            tmem_wait_ld();
-            if (cc + 1 < kTok / 32) tmem_ld32(trow + 32 * (cc + 1), buf[half ^ 1]);
-            const float2 ks = *reinterpret_cast<const float2 *>(scl + 2 * cc);
-            const float2 vs = *reinterpret_cast<const float2 *>(scl + 8 + 2 * cc);
+        for (int c = 0; c < 32; c += 2) {
+            const float k = c < 16 ? ks.x : ks.y;
+            const float2 x =
+                __fmul2_rn(make_float2(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), make_float2(k, k));
+            sr[c] = __float_as_uint(x.x);
+            sr[c + 1] = __float_as_uint(x.y);
+        }
+        if (!whole) {  // masked after the factor: a scale of 0 would turn a masked -inf into NaN
 #pragma unroll
-            for (int c = 0; c < 32; c += 2) {
-                const float k = c < 16 ? ks.x : ks.y;
-                const float2 x =
-                    __fmul2_rn(make_float2(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), make_float2(k, k));
-                sr[c] = __float_as_uint(x.x);
-                sr[c + 1] = __float_as_uint(x.y);
-            }
-            if (!whole) {  // masked after the factor: a scale of 0 would turn a masked -inf into NaN
+            for (int c = 0; c < 32; ++c)
+                if (32 * cc + c > hi_c || 32 * cc + c < lo_c) sr[c] = __float_as_uint(-INFINITY);
+        }
+        float top[4];
 #pragma unroll
-                for (int c = 0; c < 32; ++c)
-                    if (32 * cc + c > hi_c || 32 * cc + c < lo_c) sr[c] = __float_as_uint(-INFINITY);
-            }
-            float top[4];
-#pragma unroll
-            for (int v = 0; v < 4; ++v)
-                top[v] = fmax3(__uint_as_float(sr[8 * v]), __uint_as_float(sr[8 * v + 1]),
-                               fmax3(__uint_as_float(sr[8 * v + 2]), __uint_as_float(sr[8 * v + 3]),
-                                     fmax3(__uint_as_float(sr[8 * v + 4]), __uint_as_float(sr[8 * v + 5]),
-                                           fmaxf(__uint_as_float(sr[8 * v + 6]), __uint_as_float(sr[8 * v + 7])))));
-            const float most = fmaxf(fmax3(top[0], top[1], top[2]), top[3]);
-            const bool over = most > m_used + kLead || (m_used == -INFINITY && most > -INFINITY);
-            if (__any_sync(0xffffffffu, over)) {
-                const float m_new = over ? fmaxf(m_used, most) : m_used;
-                const float alpha = over ? fast_exp2(m_used - m_new) : 1.f;
-                m_used = m_new;
-                lsum *= alpha;
-                sum.x *= alpha;
-                sum.y *= alpha;
-                if (cc > 0) tmem_wait_st();  // the earlier parts of P have been written
+        for (int v = 0; v < 4; ++v)
+            top[v] = fmax3(__uint_as_float(sr[8 * v]), __uint_as_float(sr[8 * v + 1]),
+                           fmax3(__uint_as_float(sr[8 * v + 2]), __uint_as_float(sr[8 * v + 3]),
+                                 fmax3(__uint_as_float(sr[8 * v + 4]), __uint_as_float(sr[8 * v + 5]),
+                                       fmaxf(__uint_as_float(sr[8 * v + 6]), __uint_as_float(sr[8 * v + 7])))));
+        const float most = fmaxf(fmax3(top[0], top[1], top[2]), top[3]);
+        const bool over = most > m_used + kLead || (m_used == -INFINITY && most > -INFINITY);
+        if (__any_sync(0xffffffffu, over)) {
+            const float m_new = over ? fmaxf(m_used, most) : m_used;
+            const float alpha = over ? fast_exp2(m_used - m_new) : 1.f;
+            m_used = m_new;
+            lsum *= alpha;
+            sum.x *= alpha;
+            sum.y *= alpha;
+            if (cc > 0) tmem_wait_st();  // the earlier parts of P have been written
 #pragma unroll 1
-                for (int i8 = 0; i8 < 2 * cc; ++i8) {  // 16 keys: eight columns of hi, eight of lo
-                    const uint32_t c0 = (uint32_t)(i8 >> 1) * 32u + (uint32_t)(i8 & 1) * 8u;
-                    uint32_t h[8], l[8];
-                    tmem_ld8(trow + c0, h);
-                    tmem_ld8(trow + c0 + 16, l);
+            for (int i8 = 0; i8 < 2 * cc; ++i8) {  // 16 keys: eight columns of hi, eight of lo
+                const uint32_t c0 = (uint32_t)(i8 >> 1) * 32u + (uint32_t)(i8 & 1) * 8u;
+                uint32_t h[8], l[8];
+                tmem_ld8(trow + c0, h);
+                tmem_ld8(trow + c0 + 16, l);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float2 a = unpack2<__nv_bfloat16>(h[i]), b = unpack2<__nv_bfloat16>(l[i]);
+                    split_bf16((a.x + b.x) * alpha, (a.y + b.y) * alpha, h[i], l[i]);
+                }
+                tmem_st8(trow + c0, h);
+                tmem_st8(trow + c0 + 16, l);
+            }
+            if (has_o) {
+#pragma unroll 1
+                for (int c0 = 0; c0 < D; c0 += 8) {
+                    uint32_t o[8];
+                    tmem_ld8(trow + 128 + c0, o);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float2 a = unpack2<__nv_bfloat16>(h[i]), b = unpack2<__nv_bfloat16>(l[i]);
-                        split_bf16((a.x + b.x) * alpha, (a.y + b.y) * alpha, h[i], l[i]);
-                    }
-                    tmem_st8(trow + c0, h);
-                    tmem_st8(trow + c0 + 16, l);
-                }
-                if (has_o) {
-#pragma unroll 1
-                    for (int c0 = 0; c0 < D; c0 += 8) {
-                        uint32_t o[8];
-                        tmem_ld8(trow + 128 + c0, o);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-                        tmem_st8(trow + 128 + c0, o);
-                    }
+                    for (int i = 0; i < 8; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                    tmem_st8(trow + 128 + c0, o);
                 }
             }
-            // a row that has met no key yet: every score and m_used are -inf, p = 0
-            const float neg_m = m_used == -INFINITY ? -INFINITY : -m_used;
-            uint32_t ph[16], pl[16];
-#pragma unroll
-            for (int c = 0; c < 32; c += 2) {
-                const float v = c < 16 ? vs.x : vs.y;
-                const float2 x = __fadd2_rn(make_float2(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])),
-                                            make_float2(neg_m, neg_m));
-                const float2 pr = make_float2(fast_exp2(x.x), fast_exp2(x.y));
-                sum = __fadd2_rn(sum, pr);
-                const float2 pv = __fmul2_rn(pr, make_float2(v, v));
-                split_bf16(pv.x, pv.y, ph[c / 2], pl[c / 2]);
-            }
-            tmem_st16(trow + 32 * cc, ph);
-            tmem_st16(trow + 32 * cc + 16, pl);
         }
+        // a row that has met no key yet: every score and m_used are -inf, p = 0
+        const float neg_m = m_used == -INFINITY ? -INFINITY : -m_used;
+        uint32_t ph[16], pl[16];
+#pragma unroll
+        for (int c = 0; c < 32; c += 2) {
+            const float v = c < 16 ? vs.x : vs.y;
+            const float2 x = __fadd2_rn(make_float2(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])),
+                                        make_float2(neg_m, neg_m));
+            const float2 pr = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+            sum = __fadd2_rn(sum, pr);
+            const float2 pv = __fmul2_rn(pr, make_float2(v, v));
+            split_bf16(pv.x, pv.y, ph[c / 2], pl[c / 2]);
+        }
+        tmem_st16(trow + 32 * cc, ph);
+        tmem_st16(trow + 32 * cc + 16, pl);
     }
     lsum += sum.x + sum.y;
 }
@@ -453,11 +445,9 @@ struct TcItem {
 
 // I8: the pools hold int8 codes with a scale per block and KV head.  The
 // products run on the codes, which are exact as 16-bit values: K in the query's
-// type, V in bf16.  Warps 12-15 read the codes through the block table,
-// convert them in registers and write the swizzled tiles that TMA writes
-// otherwise (asynchronous copies of the next step's codes into the thread's own
-// shared memory, refilled slot by slot), and leave the tile's 8 + 8 scales in a ring of
-// their own.  The softmax warps multiply the scores by their block's K scale
+// type, V in bf16.  The producer stages the codes (TMA) and leaves the tile's
+// 8 + 8 scales in a ring of their own; warps 12-15 convert the codes in
+// registers and write the swizzled tiles that TMA writes otherwise.  The softmax warps multiply the scores by their block's K scale
 // in binary32 and the weights by its V scale before they are split into a
 // bf16 hi + lo pair, whose exponent range holds any scale.
 template <int D, typename T, bool I8 = false>
@@ -482,7 +472,7 @@ __global__ void __launch_bounds__(Regs<I8>::kThreads, 1)
     // 32c + 31 (bf16): columns whose scores have already been read.
     constexpr bool LO = BF || I8;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ uint64_t bars[2 + 4 * S + 3 * kTiles + 4 + 1];
+    __shared__ uint64_t bars[2 + 4 * S + 3 * kTiles + 4 + 1 + (I8 ? 4 : 0)];
     __shared__ TcItem s_item[2];
     __shared__ uint32_t s_tmem;
     __shared__ volatile int s_abort;
@@ -506,6 +496,7 @@ __global__ void __launch_bounds__(Regs<I8>::kThreads, 1)
     uint64_t *item_full = &bars[2 + 4 * S + 3 * kTiles];
     uint64_t *item_empty = item_full + 2;
     uint64_t *fin = item_full + 4;  // abort path: completion of every MMA issued
+    uint64_t *code_full = fin + 1, *code_empty = fin + 3;  // int8: codes of K [0] and V [1] staged, converted
     auto s_full = [&](int u) { return tile_bars + u * 3; };
     auto p_full = [&](int u) { return tile_bars + u * 3 + 1; };
     auto o_done = [&](int u) { return tile_bars + u * 3 + 2; };
@@ -535,6 +526,12 @@ __global__ void __launch_bounds__(Regs<I8>::kThreads, 1)
             mbar_init(&item_empty[i], 1 + 2 * 4 + (I8 ? 4 : 0));  // the MMA, softmax (and converting) warps
         }
         mbar_init(fin, 1);
+        if constexpr (I8) {
+            for (int i = 0; i < 2; ++i) {
+                mbar_init(&code_full[i], 1);
+                mbar_init(&code_empty[i], 4);
+            }
+        }
         fence_barrier_init();
     }
     if (warp == 1) {
@@ -562,10 +559,8 @@ __global__ void __launch_bounds__(Regs<I8>::kThreads, 1)
         const uint64_t pol_kv = policy_evict_last();  // re-read by the other q tiles of the chunk
         if (lane == 0) {
             prefetch_tensormap(&tmq);
-            if constexpr (!I8) {
-                prefetch_tensormap(&tmk);
-                prefetch_tensormap(&tmv);
-            }
+            prefetch_tensormap(&tmk);
+            prefetch_tensormap(&tmv);
         }
         const int box = p.box_rows;
         const int32_t *tables = p.tables;
@@ -720,6 +715,71 @@ __global__ void __launch_bounds__(Regs<I8>::kThreads, 1)
                         tma_load_3d(sv + dst_off, &tmv, &v_full[stage], 0, item.kvh * HALVES + lane % HALVES, row, pol_kv);
                     ++issued_v;
                 }
+            } else {
+                // codes of 128 tokens of K and of V, in boxes of box rows x 128 codes (lane t: box t),
+                // and the factors of the step's eight sub-blocks (lane i: sub-block i).  Sub-blocks
+                // without a key of the item are not loaded: what the staging holds there is
+                // finite, its factors are 0, and its scores are masked.
+                const int32_t *trow = tables + (int64_t)item.s * p.max_blocks;
+                const int lim_first = p.causal ? item.kv_len - item.q_len + item.q00 : item.kv_len - 1;
+                const int first_key = p.window > 0 ? max(0, lim_first - p.window + 1) : 0;
+                auto used = [&](int tok, int n) { return tok < item.kv_len && tok + n > first_key; };
+                // table entries, one step ahead: of lane's box, and of lane's sub-block
+                int nbox = 0, nsub = 0;
+                auto lookup = [&](int j) {
+                    nbox = nsub = -1;
+                    if (j >= nt) return;
+                    const int t0 = (item.j_first + j) * kTok;
+                    if (lane * box < kTok && used(t0 + lane * box, box)) nbox = trow[(t0 + lane * box) / p.block_size];
+                    if (lane < 8 && used(t0 + lane * 16, 16)) nsub = trow[(t0 + lane * 16) / p.block_size];
+                };
+                auto checked = [&](int phys) {
+                    if (phys >= 0 && phys < p.num_blocks) return phys;
+                    set_err(p.err, PKV_DEVERR_BLOCK);
+                    return 0;
+                };
+                lookup(0);
+                for (int j = 0; j < nt; ++j, ++gs) {
+                    const int t0 = (item.j_first + j) * kTok;
+                    const bool mine = lane * box < kTok && used(t0 + lane * box, box);
+                    int row = 0;
+                    if (mine) {
+                        const int tok = t0 + lane * box;
+                        row = checked(nbox) * p.block_size + tok % p.block_size;
+                    }
+                    float ks = 0.f, vs = 0.f;
+                    if (lane < 8 && used(t0 + lane * 16, 16)) {
+                        const int64_t at = (int64_t)checked(nsub) * p.hkv + item.kvh;
+                        ks = p.k_scale[at] * p.scale_log2;
+                        vs = p.v_scale[at];
+                    }
+                    lookup(j + 1);
+                    const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, mine)) * box * 128;
+#pragma unroll
+                    for (int which = 0; which < 2; ++which) {
+                        int okw = 1;
+                        if (lane == 0) okw = wait_phase(&code_empty[which], (gs & 1) ^ 1, &s_abort);
+                        if (!__shfl_sync(0xffffffffu, okw, 0)) {
+                            ok = false;
+                            break;
+                        }
+                        if (which == 0 && lane < 8) {
+                            s_scales[I8 ? gs & 3 : 0][lane] = ks;
+                            s_scales[I8 ? gs & 3 : 0][8 + lane] = vs;
+                        }
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_expect_tx(&code_full[which], bytes);
+                        __syncwarp();
+                        if (mine)
+                            tma_load_3d(s_codes + which * (kCodeBytes / 2) + lane * box * 128, which ? &tmv : &tmk,
+                                        &code_full[which], 0, row, item.kvh, pol_kv);
+                        if (which)
+                            ++issued_v;
+                        else
+                            ++issued_k;
+                    }
+                    if (!ok) break;
+                }
             }
         }
         if (!ok && lane == 0) {
@@ -728,10 +788,15 @@ __global__ void __launch_bounds__(Regs<I8>::kThreads, 1)
             set_err(p.err, PKV_DEVERR_TIMEOUT);
             volatile int never = 0;
             if (q_issued > 0) mbar_wait(q_full, (q_issued - 1) & 1, &never);
-            for (int k = issued_k > S ? issued_k - S : 0; k < issued_k; ++k)
-                mbar_wait(&k_full[k % S], (k / S) & 1, &never);
-            for (int k = issued_v > S ? issued_v - S : 0; k < issued_v; ++k)
-                mbar_wait(&v_full[k % S], (k / S) & 1, &never);
+            if constexpr (I8) {
+                if (issued_k > 0) mbar_wait(&code_full[0], (issued_k - 1) & 1, &never);
+                if (issued_v > 0) mbar_wait(&code_full[1], (issued_v - 1) & 1, &never);
+            } else {
+                for (int k = issued_k > S ? issued_k - S : 0; k < issued_k; ++k)
+                    mbar_wait(&k_full[k % S], (k / S) & 1, &never);
+                for (int k = issued_v > S ? issued_v - S : 0; k < issued_v; ++k)
+                    mbar_wait(&v_full[k % S], (k / S) & 1, &never);
+            }
         }
     } else if (warp == 1) {
         // ===== MMA issuer: the whole warp walks the loop, one elected lane issues =====
@@ -847,108 +912,46 @@ __global__ void __launch_bounds__(Regs<I8>::kThreads, 1)
         // ===== int8: codes to 16-bit tiles =====
         // thread = 16 codes (col) of row r16 of every 16-token sub-block of a tile
         const int col = tid & 7, r16 = (tid & 127) >> 3;
-        const int64_t pitch = (int64_t)p.hkv * D;
         const uint32_t sk_a = smem_u32(sk), sv_a = smem_u32(sv);
-        constexpr int SUBS = kTok / 16, CONV = 2;  // sub-blocks of a tile; converted at a time
-        const uint32_t k_slot = smem_u32(s_codes) + (tid & 127) * 16, v_slot = k_slot + kCodeBytes / 2;
+        const uint32_t codes = smem_u32(s_codes) + r16 * 128 + ((col ^ (r16 & 7)) << 4);  // 128-byte swizzle
+        constexpr int SUBS = kTok / 16;  // sub-blocks of a tile
         int gs = 0;  // ring position
         bool ok = true;
+        auto wait = [&](uint64_t *bar, uint32_t parity) { return __all_sync(0xffffffffu, wait_phase(bar, parity, &s_abort)); };
         for (int it = 0; ok; ++it) {
-            ok = __all_sync(0xffffffffu, wait_phase(&item_full[it & 1], (it >> 1) & 1, &s_abort));
+            ok = wait(&item_full[it & 1], (it >> 1) & 1);
             if (!ok) break;
-            const TcItem item = s_item[it & 1];
+            const int nt = max(s_item[it & 1].nt0, s_item[it & 1].nt1);
+            const bool end = s_item[it & 1].nt0 < 0;
             __syncwarp();
             if (lane == 0) mbar_arrive(&item_empty[it & 1]);
-            if (item.nt0 < 0) break;
-            const int nt = max(item.nt0, item.nt1);
-            const int32_t *trow = p.tables + (int64_t)item.s * p.max_blocks;
-            const int64_t off = (int64_t)item.kvh * D + (int64_t)r16 * pitch + col * 16;
-            // the first key of any of the item's rows (a window): earlier sub-blocks are not read
-            const int lim_first = p.causal ? item.kv_len - item.q_len + item.q00 : item.kv_len - 1;
-            const int first_key = p.window > 0 ? lim_first - p.window + 1 : 0;
-            // lane i < 8: block and pool row of sub-block i of step j, -1 where no row of the item has a key
-            int phys = -1, row = -1;
-            auto lookup = [&](int j) {
-                phys = row = -1;
-                const int tok = (item.j_first + j) * kTok + lane * 16;
-                if (j >= nt || lane >= SUBS || tok >= item.kv_len || tok + 15 < first_key) return;
-                const int lb = tok / p.block_size;
-                phys = trow[lb];
-                if (phys < 0 || phys >= p.num_blocks) {
-                    set_err(p.err, PKV_DEVERR_BLOCK);
-                    phys = 0;
-                }
-                row = phys * p.block_size + (tok - lb * p.block_size);
-            };
-            // this thread's codes of sub-block i, K or V, of the next step: into its own 16 bytes
-            auto fetch = [&](const int8_t *pool, uint32_t slot, int i) {
-                const int rr = __shfl_sync(0xffffffffu, row, i);
-                const int8_t *src = pool + (rr >= 0 ? rr * pitch + off : 0);
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(slot + i * 2048), "l"(src),
-                             "r"(rr >= 0 ? 16 : 0)
-                             : "memory");
-            };
-            float ks = 0.f, vs = 0.f;  // warp 12, lane i < 8: the factors of sub-block i of the next step
-            auto load_scales = [&] {
-                ks = vs = 0.f;
-                if (warp == 12 && phys >= 0) {
-                    ks = p.k_scale[(int64_t)phys * p.hkv + item.kvh] * p.scale_log2;
-                    vs = p.v_scale[(int64_t)phys * p.hkv + item.kvh];
-                }
-            };
-            lookup(0);
-            load_scales();
-            for (int i = 0; i < SUBS; ++i) fetch(p.kq, k_slot, i);
-            asm volatile("cp.async.commit_group;" ::: "memory");
-            for (int i = 0; i < SUBS; ++i) fetch(p.vq, v_slot, i);
-            asm volatile("cp.async.commit_group;" ::: "memory");
+            if (end) break;
             for (int j = 0; j < nt; ++j, ++gs) {
-                ok = __all_sync(0xffffffffu, wait_phase(&k_empty[gs % SK], ((gs / SK) & 1) ^ 1, &s_abort));
+                ok = wait(&k_empty[gs % SK], ((gs / SK) & 1) ^ 1) && wait(&code_full[0], gs & 1);
                 if (!ok) break;
-                if (warp == 12 && lane < SUBS) {
-                    s_scales[I8 ? gs & 3 : 0][lane] = ks;
-                    s_scales[I8 ? gs & 3 : 0][8 + lane] = vs;
-                }
-                lookup(j + 1);
-                load_scales();
-                // not unrolled, here and below: four warps on code of their own beside the
-                // softmax's would run out of instruction cache
-                asm volatile("cp.async.wait_group 1;" ::: "memory");
+                // not unrolled, here and below, for the instruction cache (two sub-blocks at a
+                // time 440 us, four 448, one 420)
 #pragma unroll 1
-                for (int i = 0; i < SUBS; i += CONV) {
-                    uint4 v[CONV];
-#pragma unroll
-                    for (int e = 0; e < CONV; ++e) v[e] = ld_shared_u4(k_slot + (i + e) * 2048);
-#pragma unroll
-                    for (int e = 0; e < CONV; ++e)
-                        store_codes<T>(sk_a + (gs % SK) * KVSTAGE, KVHALF, (i + e) * 16 + r16, col, v[e]);
-#pragma unroll
-                    for (int e = 0; e < CONV; ++e) fetch(p.kq, k_slot, i + e);
-                }
-                asm volatile("cp.async.commit_group;" ::: "memory");
+                for (int i = 0; i < SUBS; ++i)
+                    store_codes<T>(sk_a + (gs % SK) * KVSTAGE, KVHALF, i * 16 + r16, col, ld_shared_u4(codes + i * 2048));
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&k_full[gs % SK]);
-                ok = __all_sync(0xffffffffu, wait_phase(&v_empty[gs % S], ((gs / S) & 1) ^ 1, &s_abort));
-                if (!ok) break;
-                asm volatile("cp.async.wait_group 1;" ::: "memory");
-#pragma unroll 1
-                for (int i = 0; i < SUBS; i += CONV) {
-                    uint4 v[CONV];
-#pragma unroll
-                    for (int e = 0; e < CONV; ++e) v[e] = ld_shared_u4(v_slot + (i + e) * 2048);
-#pragma unroll
-                    for (int e = 0; e < CONV; ++e)
-                        store_codes<TP>(sv_a + (gs % S) * KVSTAGE, KVHALF, (i + e) * 16 + r16, col, v[e]);
-#pragma unroll
-                    for (int e = 0; e < CONV; ++e) fetch(p.vq, v_slot, i + e);
+                if (lane == 0) {
+                    mbar_arrive(&k_full[gs % SK]);
+                    mbar_arrive(&code_empty[0]);
                 }
-                asm volatile("cp.async.commit_group;" ::: "memory");
+                ok = wait(&v_empty[gs % S], ((gs / S) & 1) ^ 1) && wait(&code_full[1], gs & 1);
+                if (!ok) break;
+#pragma unroll 1
+                for (int i = 0; i < SUBS; ++i)
+                    store_codes<TP>(sv_a + (gs % S) * KVSTAGE, KVHALF, i * 16 + r16, col, ld_shared_u4(codes + kCodeBytes / 2 + i * 2048));
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&v_full[gs % S]);
+                if (lane == 0) {
+                    mbar_arrive(&v_full[gs % S]);
+                    mbar_arrive(&code_empty[1]);
+                }
             }
-            asm volatile("cp.async.wait_all;" ::: "memory");  // (nothing but zeros is in flight behind the last step)
         }
         if (!ok && lane == 0) {
             s_abort = 1;
@@ -1321,6 +1324,11 @@ static pkv_status launch_prefill_tc_t(const CUtensorMap &mq, const CUtensorMap &
     return launch_pdl(kern, grid, dim3(Regs<I8>::kThreads), (size_t)smem, stream, mq, mk, mv, mo, p);
 }
 
+// Rows per K/V TMA box: the largest of 128, 64, 32, 16 that divides the block.
+static int pool_box_rows(int block_size) {
+    return block_size % 128 == 0 ? 128 : block_size % 64 == 0 ? 64 : block_size % 32 == 0 ? 32 : 16;
+}
+
 // Prefill chunks of a varlen call on tcgen05 (rows of q_len == 1 are left to the decode kernel).
 pkv_status run_prefill_tc(const void *q, int64_t q_stride, const pkv_cache *cache, const int32_t *tables,
                           int32_t max_blocks, const int32_t *cu_q, const int32_t *seq_lens, int32_t num_seqs,
@@ -1346,10 +1354,7 @@ pkv_status run_prefill_tc(const void *q, int64_t q_stride, const pkv_cache *cach
     const int rows = 128 / p.group;
     p.q_tiles = (max_q_len + kTiles * rows - 1) / (kTiles * rows);
     p.num_seqs = num_seqs;
-    p.box_rows = cache->block_size % 128 == 0  ? 128
-                 : cache->block_size % 64 == 0 ? 64
-                 : cache->block_size % 32 == 0 ? 32
-                                               : 16;
+    p.box_rows = pool_box_rows(cache->block_size);
     p.q = q;
     p.q_stride = q_stride;
     CUtensorMap mq, mk, mv;
@@ -1406,21 +1411,23 @@ pkv_status run_prefill_i8(const void *q, int64_t q_stride, const pkv_cache_i8 *c
     p.num_seqs = num_seqs;
     p.q = q;
     p.q_stride = q_stride;
-    p.kq = cache->k;
-    p.vq = cache->v;
+    p.box_rows = pool_box_rows(cache->block_size);
     p.k_scale = cache->k_scale;
     p.v_scale = cache->v_scale;
-    CUtensorMap mq, mo, none;
-    memset(&none, 0, sizeof(none));
+    CUtensorMap mq, mk, mv, mo;
     pkv_status st = encode_q_map(&mq, q, q_stride, total_q, num_q_heads, cache->head_dim, rows, cache->dtype);
+    if (st != PKV_OK) return st;
+    st = encode_pool_rows_map_i8(&mk, cache->k, cache, 1, p.box_rows);
+    if (st != PKV_OK) return st;
+    st = encode_pool_rows_map_i8(&mv, cache->v, cache, 1, p.box_rows);
     if (st != PKV_OK) return st;
     const int wrows = rows < 32 ? rows : 32;
     st = encode_out_map(&mo, out, total_q, num_q_heads, cache->head_dim, out_dtype, out_dtype == PKV_F32 ? 16 : 32, wrows,
                         32 / wrows);
     if (st != PKV_OK) return st;
     p.out_tma = 1;
-    return cache->dtype == PKV_BF16 ? launch_prefill_tc_t<128, __nv_bfloat16, true>(mq, none, none, mo, p, num_seqs, stream)
-                                    : launch_prefill_tc_t<128, __half, true>(mq, none, none, mo, p, num_seqs, stream);
+    return cache->dtype == PKV_BF16 ? launch_prefill_tc_t<128, __nv_bfloat16, true>(mq, mk, mv, mo, p, num_seqs, stream)
+                                    : launch_prefill_tc_t<128, __half, true>(mq, mk, mv, mo, p, num_seqs, stream);
 }
 
 }  // namespace pkv
