@@ -41,9 +41,15 @@ __all__ = [
 _DT = {torch.float16: PKV_F16, torch.bfloat16: PKV_BF16, torch.float32: PKV_F32}
 
 
-def _stream(stream) -> ctypes.c_void_p:
+# the current stream's handle without building a torch.cuda.Stream (0.1 against 3 us per call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream(stream) -> int:
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(torch.cuda.current_device())
     s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    return s.cuda_stream
 
 
 def _cuda(t: torch.Tensor, name: str) -> None:
@@ -51,8 +57,8 @@ def _cuda(t: torch.Tensor, name: str) -> None:
         raise TypeError(f"{name} must be a CUDA tensor")
 
 
-def _ptr(t: Optional[torch.Tensor]):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
+    return None if t is None else t.data_ptr()
 
 
 def _cache(k_cache: torch.Tensor, v_cache: torch.Tensor) -> PkvCache:
@@ -102,10 +108,9 @@ def _on_current_device(**tensors: Optional[torch.Tensor]) -> None:
     """Every given tensor lies on the current CUDA device (where the call's stream is)."""
     dev = torch.cuda.current_device()
     for name, t in tensors.items():
-        if t is not None:
+        if t is not None and (not isinstance(t, torch.Tensor) or t.get_device() != dev):
             _cuda(t, name)
-            if t.device.index != dev:
-                raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
+            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
 
 
 def _check_err(err: Optional[torch.Tensor]) -> None:

@@ -82,10 +82,14 @@ constexpr int kMinSubBlocksPerCta = 4;
 // so no sequence is cut and the merge has nothing to combine.
 constexpr int kWholeSeqMaxSeqs = 32;
 constexpr int kWholeSeqMaxSubBlocks = 64;
+// The decode rows of a packed int8 call: a CTA takes ~1.5 us per int8 sub-block
+// when it runs alone, so a handful of short rows is cut earlier.
+constexpr int kWholeSeqMaxPackedI8 = 16;
 // The one test of that split, shared by the host (with its bound on the
 // sub-blocks), the decode kernel and the merge (with the actual count).
-__host__ __device__ __forceinline__ bool whole_seq_split(int64_t sub_blocks, int64_t num_seqs, int64_t grid_x) {
-    return sub_blocks <= kWholeSeqMaxSubBlocks && num_seqs <= kWholeSeqMaxSeqs && num_seqs <= grid_x;
+__host__ __device__ __forceinline__ bool whole_seq_split(int64_t sub_blocks, int64_t num_seqs, int64_t grid_x,
+                                                         int64_t max_sub_blocks) {
+    return sub_blocks <= max_sub_blocks && num_seqs <= kWholeSeqMaxSeqs && num_seqs <= grid_x;
 }
 
 struct DecodeParams {
@@ -105,6 +109,7 @@ struct DecodeParams {
     int32_t *ws_meta;              // [0] total sub-blocks, [1] CTAs used, [2 + s] first sub-block of s
     int32_t cmax;                  // gridDim.x at most (the records' CTA stride)
     int32_t grid_x;                // the decode launch's gridDim.x (the merge recomputes the split with it)
+    int32_t whole_max;             // sub-blocks up to which the small-call split applies
     int32_t *err;
     int32_t stages;
     int32_t window;                // > 0: attend only the last `window` keys
@@ -120,7 +125,7 @@ struct DecodeParams {
     float *key_w;                  // accumulated weights, key (s, h, t) at s * w_seq + h * w_head + t
     int64_t w_seq, w_head;
     float *scores;                 // workspace [num_seqs][hkv][max_blocks * block_size][group], in base 2
-    float2 *norm;                  // workspace [num_seqs][hq]: (max, 1 / sum) of a row's softmax
+    float2 *norm;                  // workspace [num_seqs][hq]: (max, 1 / sum) of rows finished by the decode kernel
 };
 
 // First key a decode row of a sequence with L keys attends (sliding window).
@@ -229,7 +234,7 @@ constexpr float kLazyMax = 8.f;
 // AP: append mode (pkv_attn_decode_append), W: key weights
 // (pkv_attn_decode_weights), each compiled separately so that the plain
 // decode carries none of their code.  W leaves every score and, per finished
-// row, the softmax's max and sum in the workspace for key_weights_kernel.
+// row, the softmax's max and sum in the workspace for add_key_weights.
 template <int D, typename T, bool I8, bool AP = false, bool W = false>
 __global__ void __launch_bounds__(cta_threads<D, I8>(), I8 ? kI8CtasPerSm : (D == 64 ? kD64CtasPerSm : 1))
     decode_splitk_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
@@ -279,7 +284,7 @@ __global__ void __launch_bounds__(cta_threads<D, I8>(), I8 ? kI8CtasPerSm : (D =
         }
         total += chunk;
     }
-    const bool whole = whole_seq_split(total, p.num_seqs, gridDim.x);
+    const bool whole = whole_seq_split(total, p.num_seqs, gridDim.x, p.whole_max);
     const int64_t want = (total + kMinSubBlocksPerCta - 1) / kMinSubBlocksPerCta;
     const int ctas = whole ? p.num_seqs : (int)(want < gridDim.x ? want : gridDim.x);
     if (blockIdx.x >= ctas && !meta_cta) return;
@@ -903,12 +908,11 @@ constexpr int kMergeThreads = 256;
 // -> 0.2007; A/B, one box).
 constexpr int kMergeScanMaxSeqs = 1024;
 
-template <int D, typename T, int kMergeHeads, bool W = false>
-__global__ void __launch_bounds__(kMergeThreads) decode_merge_kernel(const DecodeParams p) {
+template <int D, typename T, int kMergeHeads>
+__device__ __forceinline__ void merge_parts(const DecodeParams &p, const int s, const int head_group) {
     extern __shared__ float4 s_merge[];  // [groups][kMergeHeads * D / 4] partial sums, then [parts][heads] weights
     __shared__ int s_scan[32];
     __shared__ long long s_start;
-    const int s = blockIdx.x;
     // The split of the concatenated sub-blocks into CTA ranges depends only on
     // the call's inputs (lengths, row offsets, window, table width), which the
     // decode kernel read after its own dependency wait.  This grid starts only
@@ -936,7 +940,7 @@ __global__ void __launch_bounds__(kMergeThreads) decode_merge_kernel(const Decod
         n = decode_sub_blocks(p, s);
         const int64_t want = (total + kMinSubBlocksPerCta - 1) / kMinSubBlocksPerCta;
         ctas = want < p.grid_x ? want : p.grid_x;  // as the decode kernel takes it
-        whole = whole_seq_split(total, p.num_seqs, p.grid_x);
+        whole = whole_seq_split(total, p.num_seqs, p.grid_x, p.whole_max);
     }
     pdl_wait();
     pdl_trigger();
@@ -944,7 +948,7 @@ __global__ void __launch_bounds__(kMergeThreads) decode_merge_kernel(const Decod
     const int64_t qrow = p.cu_q ? (int64_t)p.cu_q[s] : (int64_t)s;
     const int G = p.group, HG = p.heads_per_cta;
     const int hq = p.hkv * G;
-    const int h0 = blockIdx.y * kMergeHeads;
+    const int h0 = head_group * kMergeHeads;
     const int nh = min(kMergeHeads, hq - h0);
     if (!early) {
         total = p.ws_meta[0];
@@ -1001,9 +1005,6 @@ __global__ void __launch_bounds__(kMergeThreads) decode_merge_kernel(const Decod
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) Lsum += __shfl_xor_sync(0xffffffffu, Lsum, off);
         const float inv = 1.f / Lsum;
-        if constexpr (W) {
-            if (lane == 0) p.norm[(int64_t)s * hq + h] = make_float2(M, inv);
-        }
         for (int c = lane; c < parts; c += 32) s_w[c * kMergeHeads + warp] *= inv;
     }
     __syncthreads();
@@ -1068,62 +1069,132 @@ __global__ void __launch_bounds__(kMergeThreads) decode_merge_kernel(const Decod
     }
 }
 
-// Adds the step's softmax weights to the accumulated ones: a thread takes one
-// key of one (sequence, KV head) and sums its weight over the group's query
-// heads, 2^(score - max) / sum with the row's max and sum, from the scores the
-// decode kernel left.  Reads 4 G + 4 and writes 4 bytes per key beside the
-// decode kernel's 4 G written; with G scores in one vector the accesses are
-// whole lines.
-constexpr int kWeightThreads = 256;
-
-template <int G>
-__global__ void __launch_bounds__(kWeightThreads) key_weights_kernel(const DecodeParams p, int chunks) {
-    pdl_wait();
-    pdl_trigger();
-    const int64_t row = blockIdx.x / chunks;   // (sequence, KV head)
-    const int t = (int)(blockIdx.x % chunks) * kWeightThreads + threadIdx.x;
-    const int64_t s = row / p.hkv;
-    const int h = (int)(row - s * p.hkv);
-    const int L = p.seq_lens[s];
-    const int64_t cap = (int64_t)p.max_blocks * p.block_size;
-    if (L > cap || t >= L || t < decode_first_key(p, L)) return;
-    const float *sp = p.scores + (row * cap + t) * G;
-    float x[G];
-    if constexpr (G == 1) {
-        x[0] = sp[0];
-    } else if constexpr (G == 2) {
-        const float2 a = *reinterpret_cast<const float2 *>(sp);
-        x[0] = a.x;
-        x[1] = a.y;
-    } else {
-#pragma unroll
-        for (int i = 0; i < G; i += 4) {
-            const float4 a = *reinterpret_cast<const float4 *>(sp + i);
-            x[i] = a.x;
-            x[i + 1] = a.y;
-            x[i + 2] = a.z;
-            x[i + 3] = a.w;
-        }
-    }
-    float sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < G; ++i) {
-        const float2 nm = p.norm[row * G + i];
-        sum += fast_exp2(x[i] - nm.x) * nm.y;
-    }
-    p.key_w[s * p.w_seq + h * p.w_head + t] += sum;
+template <int D, typename T, int kMergeHeads>
+__global__ void __launch_bounds__(kMergeThreads) decode_merge_kernel(const DecodeParams p) {
+    merge_parts<D, T, kMergeHeads>(p, blockIdx.x, blockIdx.y);
 }
 
-static pkv_status launch_key_weights(const DecodeParams &p, cudaStream_t stream) {
+// Adds the step's softmax weights to the accumulated ones: a CTA takes
+// kWeightKeys keys of one (sequence, KV head), a thread every 256th of them, and
+// sums a key's weight over the group's query heads, 2^(score - max) / sum, from
+// the scores the decode kernel left.  The row's max and sum come from the
+// decode kernel, or, for a sequence cut over several of its CTAs, from their
+// records: each CTA joins them itself (a warp per head), so that the keys need
+// not wait for the merge.  Reads 4 G + 4 and writes 4 bytes per key beside the
+// decode kernel's 4 G written.
+constexpr int kWeightThreads = kMergeThreads;
+constexpr int kWeightsPerThread = 8;  // 2, 4, 8: GQA 32/8 batch of 256 427, 417, 413 us; long 197, 187, 184
+constexpr int kWeightKeys = kWeightThreads * kWeightsPerThread;
+
+template <int G>
+__device__ __forceinline__ void add_key_weights(const DecodeParams &p, int64_t row, int chunk) {
+    __shared__ float2 s_norm[G];
+    const int64_t s = row / p.hkv;
+    const int h = (int)(row - s * p.hkv);
+    const int tid = threadIdx.x;
+    pdl_wait();
+    pdl_trigger();
+    // two rounds of loads: the lengths and the split, then scores, weights and records
+    const int L = p.seq_lens[s];
+    const int64_t total = p.ws_meta[0], ctas = p.ws_meta[1], start = p.ws_meta[2 + s], n = p.ws_meta[3 + s] - start;
     const int64_t cap = (int64_t)p.max_blocks * p.block_size;
-    const int64_t chunks = (cap + kWeightThreads - 1) / kWeightThreads;
-    const int64_t ctas = chunks * p.num_seqs * p.hkv;
+    const int first = decode_first_key(p, L);
+    const int t0 = chunk * kWeightKeys;
+    if (L > cap || t0 >= L || t0 + kWeightKeys <= first) return;
+    const float *sp = p.scores + row * cap * G;
+    float *w = p.key_w + s * p.w_seq + h * p.w_head;
+    float x[kWeightsPerThread][G], old[kWeightsPerThread];
+#pragma unroll
+    for (int u = 0; u < kWeightsPerThread; ++u) {
+        const int t = t0 + u * kWeightThreads + tid;
+        if (t >= L || t < first) continue;
+        old[u] = w[t];
+        const float *xp = sp + (int64_t)t * G;
+        if constexpr (G == 1) {
+            x[u][0] = xp[0];
+        } else if constexpr (G == 2) {
+            const float2 a = *reinterpret_cast<const float2 *>(xp);
+            x[u][0] = a.x;
+            x[u][1] = a.y;
+        } else {
+#pragma unroll
+            for (int i = 0; i < G; i += 4) {
+                const float4 a = *reinterpret_cast<const float4 *>(xp + i);
+                x[u][i] = a.x;
+                x[u][i + 1] = a.y;
+                x[u][i + 2] = a.z;
+                x[u][i + 3] = a.w;
+            }
+        }
+    }
+    // the row's norms, joined from the records where the sequence was cut
+    const bool whole = whole_seq_split(total, p.num_seqs, p.grid_x, p.whole_max);
+    const int c0 = whole ? 0 : range_owner(start, total, ctas), c1 = whole ? 0 : range_owner(start + n - 1, total, ctas);
+    const int warp = tid >> 5, lane = tid & 31;
+    if (warp < G) {
+        if (c0 == c1) {
+            if (lane == 0) s_norm[warp] = p.norm[row * G + warp];
+        } else {
+            const int slot0 = start == (int64_t)c0 * total / ctas ? 0 : 1;
+            const int hgi = h / p.heads_per_cta, hl = (h - hgi * p.heads_per_cta) * G + warp;
+            float M = -INFINITY, l = 0.f;
+            for (int c = c0 + lane; c <= c1; c += 32) {
+                const int64_t rec = (((int64_t)hgi * p.cmax + c) * 2 + (c == c0 ? slot0 : 0)) * (p.heads_per_cta * G) + hl;
+                const float2 ml = *reinterpret_cast<const float2 *>(p.ws_ml + rec * 2);
+                const float m = fmaxf(M, ml.x);
+                l = l * exp2f(M - m) + ml.y * exp2f(ml.x - m);
+                M = m;
+            }
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) {
+                const float m2 = __shfl_xor_sync(0xffffffffu, M, off), l2 = __shfl_xor_sync(0xffffffffu, l, off);
+                const float m = fmaxf(M, m2);
+                l = (M == -INFINITY ? 0.f : l * exp2f(M - m)) + (m2 == -INFINITY ? 0.f : l2 * exp2f(m2 - m));
+                M = m;
+            }
+            if (lane == 0) s_norm[warp] = make_float2(M, 1.f / l);
+        }
+    }
+    __syncthreads();
+    float2 nm[G];
+#pragma unroll
+    for (int i = 0; i < G; ++i) nm[i] = s_norm[i];
+#pragma unroll
+    for (int u = 0; u < kWeightsPerThread; ++u) {
+        const int t = t0 + u * kWeightThreads + tid;
+        if (t >= L || t < first) continue;
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < G; ++i) sum += fast_exp2(x[u][i] - nm[i].x) * nm[i].y;
+        w[t] = old[u] + sum;
+    }
+}
+
+// The merge and the key weights of a call in one launch: the first `merges`
+// CTAs merge (sequence fastest), the others take key_chunks chunks per row.
+template <int D, typename T, int kMergeHeads, int G>
+__global__ void __launch_bounds__(kMergeThreads) decode_finish_kernel(const DecodeParams p, const int merges,
+                                                                      const int key_chunks) {
+    if ((int)blockIdx.x < merges) {
+        merge_parts<D, T, kMergeHeads>(p, blockIdx.x % p.num_seqs, blockIdx.x / p.num_seqs);
+    } else {
+        const int i = blockIdx.x - merges;
+        add_key_weights<G>(p, i / key_chunks, i % key_chunks);
+    }
+}
+
+template <int D, typename T, int kMergeHeads>
+static pkv_status launch_finish(const DecodeParams &p, int merges, size_t smem, cudaStream_t stream) {
+    const int64_t cap = (int64_t)p.max_blocks * p.block_size;
+    const int64_t chunks = (cap + kWeightKeys - 1) / kWeightKeys;
+    const int64_t ctas = merges + chunks * p.num_seqs * p.hkv;
     if (ctas == 0) return PKV_OK;
-    auto kern = p.group == 1   ? key_weights_kernel<1>
-                : p.group == 2 ? key_weights_kernel<2>
-                : p.group == 4 ? key_weights_kernel<4>
-                               : key_weights_kernel<8>;
-    return launch_pdl(kern, dim3((unsigned)ctas), dim3(kWeightThreads), 0, stream, p, (int)chunks);
+    auto kern = p.group == 1   ? decode_finish_kernel<D, T, kMergeHeads, 1>
+                : p.group == 2 ? decode_finish_kernel<D, T, kMergeHeads, 2>
+                : p.group == 4 ? decode_finish_kernel<D, T, kMergeHeads, 4>
+                               : decode_finish_kernel<D, T, kMergeHeads, 8>;
+    return launch_pdl(kern, dim3((unsigned)ctas), dim3(kMergeThreads), smem, stream, p, merges,
+                      (int)(chunks > 0 ? chunks : 1));
 }
 
 // ---- host side -------------------------------------------------------------
@@ -1191,7 +1262,7 @@ static pkv_status launch_decode_t(const CUtensorMap &mk, const CUtensorMap &mv, 
     unsigned grid_x = (unsigned)(need < 1 ? 1 : need < pl.cmax ? need : pl.cmax);
     // a call this small even at its tables' capacity gets a CTA per sequence,
     // each taking its sequence whole (the kernels check the same bounds)
-    if (whole_seq_split(bound, p.num_seqs, pl.cmax) && (unsigned)p.num_seqs > grid_x) grid_x = (unsigned)p.num_seqs;
+    if (whole_seq_split(bound, p.num_seqs, pl.cmax, p.whole_max) && (unsigned)p.num_seqs > grid_x) grid_x = (unsigned)p.num_seqs;
     DecodeParams pg = p;
     pg.grid_x = (int32_t)grid_x;
     st = launch_pdl(kern, dim3(grid_x, pl.num_hg), dim3(pl.threads), (size_t)pl.smem_bytes, stream, mk, mv, pg);
@@ -1199,7 +1270,10 @@ static pkv_status launch_decode_t(const CUtensorMap &mk, const CUtensorMap &mv, 
     // a call the small-call split surely covers (total <= bound, grid = a CTA
     // per sequence) cuts no sequence, and its empty rows are written by the
     // decode kernel: no merge
-    if (whole_seq_split(bound, p.num_seqs, grid_x)) return W ? launch_key_weights(pg, stream) : PKV_OK;
+    if (whole_seq_split(bound, p.num_seqs, grid_x, p.whole_max)) {
+        if constexpr (W) return launch_finish<D, T, 1>(pg, 0, 0, stream);
+        return PKV_OK;
+    }
     // the merge reads only what the decode kernel wrote: launch it as a
     // programmatic dependent so it is scheduled while the decode kernel drains
     // many sequences: 8 query heads per merge CTA (fewer, mostly idle, CTAs);
@@ -1207,21 +1281,26 @@ static pkv_status launch_decode_t(const CUtensorMap &mk, const CUtensorMap &mv, 
     // that leaves SMs idle: 1
     const int hq = p.hkv * p.group;
     const int mh = p.num_seqs >= 128 ? 8 : (int64_t)p.num_seqs * ((hq + 3) / 4) >= pl.cmax * pl.num_hg ? 4 : 1;
+    const size_t merge_smem = (size_t)kMergeThreads * sizeof(float4) + (size_t)p.cmax * mh * sizeof(float);
+    if constexpr (W) {
+        const int merges = p.num_seqs * ((hq + mh - 1) / mh);
+        return mh == 8   ? launch_finish<D, T, 8>(pg, merges, merge_smem, stream)
+               : mh == 4 ? launch_finish<D, T, 4>(pg, merges, merge_smem, stream)
+                         : launch_finish<D, T, 1>(pg, merges, merge_smem, stream);
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(p.num_seqs, (hq + mh - 1) / mh);
     cfg.blockDim = dim3(kMergeThreads);
-    cfg.dynamicSmemBytes = (size_t)kMergeThreads * sizeof(float4) + (size_t)p.cmax * mh * sizeof(float);
+    cfg.dynamicSmemBytes = merge_smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    auto merge = mh == 8   ? decode_merge_kernel<D, T, 8, W>
-                 : mh == 4 ? decode_merge_kernel<D, T, 4, W>
-                           : decode_merge_kernel<D, T, 1, W>;
+    auto merge = mh == 8 ? decode_merge_kernel<D, T, 8> : mh == 4 ? decode_merge_kernel<D, T, 4> : decode_merge_kernel<D, T, 1>;
     PKV_CUDA_TRY(cudaLaunchKernelEx(&cfg, merge, pg));
-    return W ? launch_key_weights(pg, stream) : PKV_OK;
+    return PKV_OK;
 }
 
 // Workspace of the key weights behind the decode plan's: norms, then scores.
@@ -1281,6 +1360,7 @@ static pkv_status run_decode_impl(const void *q, int64_t q_stride, const pkv_cac
     p.ws_ml = reinterpret_cast<float *>(ws + pl.meta_bytes);
     p.ws_o = reinterpret_cast<float *>(ws + pl.meta_bytes + pl.ml_bytes);
     p.cmax = pl.cmax;
+    p.whole_max = kWholeSeqMaxSubBlocks;
     p.err = err_word;
     p.stages = pl.stages;
     p.window = window > 0 ? window : 0;
@@ -1370,6 +1450,7 @@ static pkv_status run_decode_i8_impl(const void *q, int64_t q_stride, const pkv_
     p.ws_ml = reinterpret_cast<float *>(ws + pl.meta_bytes);
     p.ws_o = reinterpret_cast<float *>(ws + pl.meta_bytes + pl.ml_bytes);
     p.cmax = pl.cmax;
+    p.whole_max = cu_q ? kWholeSeqMaxPackedI8 : kWholeSeqMaxSubBlocks;
     p.err = err_word;
     p.stages = pl.stages;
     p.window = window > 0 ? window : 0;
@@ -1558,7 +1639,7 @@ static pkv_status check_key_weights(const float *weights, int64_t seq_stride, in
     PKV_CHECK_ARG(keys < (int64_t)1 << 31, PKV_ERR_SHAPE, "%s: tables cover 2^31 keys or more", what);
     PKV_CHECK_ARG(head_stride >= keys && seq_stride >= (hkv - 1) * head_stride + keys, PKV_ERR_SHAPE,
                   "%s: weights rows shorter than the tables' %lld keys, or overlapping", what, (long long)keys);
-    PKV_CHECK_ARG((keys + kWeightThreads - 1) / kWeightThreads * num_seqs * hkv < (int64_t)1 << 31, PKV_ERR_UNSUPPORTED,
+    PKV_CHECK_ARG((keys / kWeightKeys + 9) * num_seqs * hkv < (int64_t)1 << 31, PKV_ERR_UNSUPPORTED,
                   "%s: num_seqs * num_kv_heads * keys too large", what);
     return PKV_OK;
 }

@@ -376,21 +376,24 @@ __device__ __forceinline__ void unit_sync(int cluster) {
 // Where row i of (sequence, head) comes from and goes to: token rows of the
 // pool, or src < 0 for a row that is not moved because its data is bad.
 struct Move {
-    int64_t src, dst;
+    int32_t src, dst;  // num_blocks * block_size < 2^31
     int32_t from;
 };
 
-__device__ __forceinline__ int64_t pool_row(const CompactParams &p, const int32_t *trow, int t) {
+__device__ __forceinline__ int32_t pool_row(const CompactParams &p, const int32_t *trow, int t) {
     const int lb = t / p.block_size;
     const int phys = trow[lb];
     if (phys < 0 || phys >= p.num_blocks) return -1;
-    return (int64_t)phys * p.block_size + (t - lb * p.block_size);
+    return phys * p.block_size + (t - lb * p.block_size);
 }
 
-__device__ __forceinline__ Move find_move(const CompactParams &p, const int32_t *kept, const int32_t *trow, int i, int L) {
+// The move of row i, or none where i is past the budget (n).
+__device__ __forceinline__ Move find_move(const CompactParams &p, const int32_t *kept, const int32_t *trow, int i, int n,
+                                          int L) {
     Move m;
+    m.from = m.src = m.dst = -1;
+    if (i >= n) return m;
     m.from = kept[i];
-    m.src = m.dst = -1;
     if (m.from < i || m.from >= L || (i > 0 && kept[i - 1] >= m.from)) {
         set_err(p.err, PKV_DEVERR_KEEP);
         m.from = -1;
@@ -405,14 +408,11 @@ __device__ __forceinline__ Move find_move(const CompactParams &p, const int32_t 
     return m;
 }
 
-__device__ __forceinline__ int64_t shfl64(int64_t x, int lane) {
-    return (int64_t)__shfl_sync(0xffffffffu, (long long)x, lane);
-}
-
 // A cluster of p.cluster CTAs (1: no cluster) per (sequence, KV head, K or V),
 // its CTAs on neighbouring chunks.  A round loads one chunk per CTA, waits for
 // the cluster, and stores: the sources of a later round lie behind every row
-// that this one writes.  RB: bytes of a head's row.
+// that this one writes, so the next round's kept positions and table entries
+// are read while this round's rows are in flight.  RB: bytes of a head's row.
 template <int RB>
 __global__ void __launch_bounds__(kMoveThreads) evict_compact_kernel(const CompactParams p) {
     constexpr int LPR = RB / 16;              // lanes per row
@@ -438,27 +438,27 @@ __global__ void __launch_bounds__(kMoveThreads) evict_compact_kernel(const Compa
     uint8_t *pool = static_cast<uint8_t *>(which ? p.v : p.k) + (int64_t)h * RB;
     const int64_t pitch = (int64_t)p.hkv * RB;
     float *w = p.w && which == 0 ? p.w + seq * p.seq_stride + h * p.head_stride : nullptr;
-    for (int base = 0; base < n; base += kChunk * p.cluster) {
-        const int c0 = base + rank * kChunk;
-        const int i = c0 + warp * kMoveRows + lane;   // the row this lane looks up (lanes 0 .. 15)
-        Move m;
-        m.src = m.dst = -1;
-        m.from = -1;
-        if (lane < kMoveRows && i < n) m = find_move(p, kept, trow, i, L);
+    // the row this lane looks up (lanes 0 .. 15)
+    int i = lane < kMoveRows ? rank * kChunk + warp * kMoveRows + lane : n;
+    const int stride = kChunk * p.cluster;
+    Move next = find_move(p, kept, trow, i, n, L);
+    for (int base = 0; base < n; base += stride, i = i < n - stride ? i + stride : n) {
+        Move m = next;
         if (m.from == i) m.src = -1;
         float wv = 0.f;
         if (w && m.from > i) wv = w[m.from];
         uint4 r[LOADS];
 #pragma unroll
         for (int u = 0; u < LOADS; ++u) {
-            const int64_t src = shfl64(m.src, u * (32 / LPR) + lane / LPR);
+            const int src = __shfl_sync(0xffffffffu, m.src, u * (32 / LPR) + lane / LPR);
             if (src >= 0) r[u] = *(reinterpret_cast<const uint4 *>(pool + src * pitch) + lane % LPR);
         }
+        next = find_move(p, kept, trow, i < n - stride ? i + stride : n, n, L);
         unit_sync(p.cluster);  // every source of the round is read
 #pragma unroll
         for (int u = 0; u < LOADS; ++u) {
             const int from = u * (32 / LPR) + lane / LPR;
-            const int64_t src = shfl64(m.src, from), dst = shfl64(m.dst, from);
+            const int src = __shfl_sync(0xffffffffu, m.src, from), dst = __shfl_sync(0xffffffffu, m.dst, from);
             if (src >= 0) *(reinterpret_cast<uint4 *>(pool + dst * pitch) + lane % LPR) = r[u];
         }
         if (w && m.from > i) w[i] = wv;
@@ -551,36 +551,55 @@ __global__ void __launch_bounds__(kMoveThreads) evict_compact_i8_kernel(const Co
     float *w = p.w && which == 0 ? p.w + seq * p.seq_stride + h * p.head_stride : nullptr;
     if (threadIdx.x < 3 * (kChunk / kMoveRows)) s_max[0][threadIdx.x] = 0u;
     __syncthreads();
-    int round = 0;
-    for (int base = 0; base < n; base += p.chunk * p.cluster, round = round == 2 ? 0 : round + 1) {
-        const int c0 = base + rank * p.chunk;
-        const int next = round == 2 ? 0 : round + 1;
-        if (threadIdx.x < kChunk / kMoveRows) s_max[next][threadIdx.x] = 0u;
-        const int local = warp * kMoveRows;             // first row of the warp in the chunk
-        const int slot = local / p.block_size;          // its block in the chunk
-        const int block_end = min(n, c0 + (slot + 1) * p.block_size);
-        const int i = c0 + local + lane;
-        const bool mine = local < p.chunk && c0 + local < n;
-        const bool moved = mine && kept[block_end - 1] != block_end - 1;
+    const int local = warp * kMoveRows;                 // first row of the warp in the chunk
+    const int slot = local / p.block_size;              // its block in the chunk
+    // round r of the unit's CTAs: the warp's rows from `row` (n: none) and whether their block changes
+    struct Ahead {
         Move m;
-        m.src = m.dst = -1;
-        m.from = -1;
-        float sc = 0.f, wv = 0.f;
-        if (moved && lane < kMoveRows && i < n) {
-            m = find_move(p, kept, trow, i, L);
-            if (m.src >= 0) sc = scales[m.src / p.block_size * p.hkv + h];
-            if (w && m.from > i) wv = w[m.from];
-        }
+        float sc;
+        int row;
+        bool moved;
+    };
+    auto look = [&](int base) -> Ahead {
+        Ahead a;
+        a.m.from = a.m.src = a.m.dst = -1;
+        a.sc = 0.f;
+        a.row = base + rank * p.chunk + local;
+        a.moved = false;
+        if (local >= p.chunk || a.row >= n) return a;
+        const int block_end = min(n, base + rank * p.chunk + (slot + 1) * p.block_size);
+        a.moved = kept[block_end - 1] != block_end - 1;
+        if (a.moved && lane < kMoveRows) a.m = find_move(p, kept, trow, a.row + lane, n, L);
+        if (a.m.src >= 0) a.sc = scales[(int64_t)(a.m.src / p.block_size) * p.hkv + h];
+        return a;
+    };
+    int round = 0;
+    const int stride = p.chunk * p.cluster;
+    Ahead next = look(0);
+    for (int base = 0; base < n; base += stride, round = round == 2 ? 0 : round + 1) {
+        const int clear = round == 2 ? 0 : round + 1;
+        if (threadIdx.x < kChunk / kMoveRows) s_max[clear][threadIdx.x] = 0u;
+        const Move m = next.m;
+        const float sc = next.sc;
+        const bool moved = next.moved;
+        const int i = next.row + lane;
+        float wv = 0.f;
+        if (w && m.from > i) wv = w[m.from];
         uint4 r[LOADS];
         float rs[LOADS];
         float top = 0.f;
+        // the rows in flight first, then the next round's positions
 #pragma unroll
         for (int u = 0; u < LOADS; ++u) {
             const int from = u * (32 / LPR) + lane / LPR;
-            const int64_t src = shfl64(m.src, from);
+            const int src = __shfl_sync(0xffffffffu, m.src, from);
             rs[u] = __shfl_sync(0xffffffffu, sc, from);
             r[u] = make_uint4(0u, 0u, 0u, 0u);
             if (src >= 0) r[u] = *(reinterpret_cast<const uint4 *>(pool + src * pitch) + lane % LPR);
+        }
+        if (base < n - stride) next = look(base + stride);
+#pragma unroll
+        for (int u = 0; u < LOADS; ++u) {
             const uint32_t m = max_codes(r[u].w, max_codes(r[u].z, max_codes(r[u].y, max_codes(r[u].x, 0u))));
             // |code| * |scale| rounds monotonically in |code|: the row's largest value
             top = fmaxf(top, __fmul_rn((float)max(m & 0xFFFFu, m >> 16), fabsf(rs[u])));
@@ -597,7 +616,7 @@ __global__ void __launch_bounds__(kMoveThreads) evict_compact_i8_kernel(const Co
 #pragma unroll
             for (int u = 0; u < LOADS; ++u) {
                 const int from = u * (32 / LPR) + lane / LPR;
-                const int64_t dst = shfl64(m.dst, from);
+                const int dst = __shfl_sync(0xffffffffu, m.dst, from);
                 if (scale > 0.f) {
                     r[u].x = requantise4(r[u].x, rs[u], scale, inv);
                     r[u].y = requantise4(r[u].y, rs[u], scale, inv);
@@ -609,7 +628,7 @@ __global__ void __launch_bounds__(kMoveThreads) evict_compact_i8_kernel(const Co
                 if (dst >= 0) *(reinterpret_cast<uint4 *>(pool + dst * pitch) + lane % LPR) = r[u];
             }
             if (lane == 0 && local % p.block_size == 0 && m.dst >= 0)
-                scales[m.dst / p.block_size * p.hkv + h] = scale;
+                scales[(int64_t)(m.dst / p.block_size) * p.hkv + h] = scale;
             if (w && m.from > i) w[i] = wv;
         }
     }
