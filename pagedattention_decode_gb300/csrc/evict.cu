@@ -345,9 +345,11 @@ pkv_status launch_cluster(void (*kernel)(KArgs...), unsigned grid, unsigned bloc
 
 // ---- moves ---------------------------------------------------------------------
 
+// 512 threads, also where 256 would do (one sequence of 131,072 keys, int8: 239
+// against 363 us: half the rows are in flight).
 constexpr int kMoveThreads = 512;
-constexpr int kMoveRows = 16;                               // rows per warp and chunk
-constexpr int kChunk = kMoveRows * kMoveThreads / 32;      // rows per chunk
+constexpr int kMoveRows = 16;                           // rows per warp and chunk
+constexpr int kChunk = kMoveRows * kMoveThreads / 32;  // rows per chunk
 
 struct CompactParams {
     void *k, *v;                 // pools
@@ -477,11 +479,17 @@ __device__ __forceinline__ void code_floats(uint32_t word, float2 &lo, float2 &h
                                 __uint_as_float(__byte_perm(x, 0x4B000000u, 0x7543u))), off);
 }
 
-// The largest |code| of a word's even and odd bytes, joined to those in `m` (16-bit lanes).
-__device__ __forceinline__ uint32_t max_codes(uint32_t word, uint32_t m) {
-    const uint32_t s = (word >> 7) & 0x01010101u;
-    const uint32_t y = (word ^ (s * 255u)) + s;  // |code| <= 128 per byte: no carry
-    return __vmaxu2(__vmaxu2(m, y & 0x00FF00FFu), (y >> 8) & 0x00FF00FFu);
+// Running maxima and minima of codes, as pairs of 16-bit integers.
+__device__ __forceinline__ void range_codes(uint32_t word, uint32_t &most, uint32_t &least) {
+    uint32_t lo, hi;  // bytes 0, 1 and 2, 3 with their signs
+    asm("prmt.b32 %0, %1, 0, 0x9180;" : "=r"(lo) : "r"(word));
+    asm("prmt.b32 %0, %1, 0, 0xB3A2;" : "=r"(hi) : "r"(word));
+    most = __vmaxs2(__vmaxs2(most, lo), hi);
+    least = __vmins2(__vmins2(least, lo), hi);
+}
+
+__device__ __forceinline__ int largest_code(uint32_t most, uint32_t least) {
+    return max(max((int)(int16_t)most, (int)most >> 16), -min((int)(int16_t)least, (int)least >> 16));
 }
 
 __device__ __forceinline__ uint32_t requantise_exact(float x, float scale) {
@@ -489,32 +497,33 @@ __device__ __forceinline__ uint32_t requantise_exact(float x, float scale) {
     return (uint32_t)(int32_t)fminf(fmaxf(r, -127.f), 127.f) & 255u;
 }
 
-// Four codes with scale `from` under the scale `to` (> 0; inv = 1 / to): code' =
-// rint(fl(fl(code * from) / to)), at most 127.  The product with inv differs
-// from that quotient by less than 127 * 3 * 2^-24 < 2^-15, so unless it lies
-// within 2^-14 of a half it rounds to the same integer; adding 1.5 * 2^23
-// rounds it and leaves the integer in the low byte.  |code'| <= 127 holds but
-// for the last bits of |x| = the largest, 127 * to, which round to 127.
-__device__ __forceinline__ uint32_t requantise4(uint32_t word, float from, float to, float inv) {
+// Four codes with scale `from` under the scale `to` (> 0; ratio = from * (1 / to)):
+// code' = rint(fl(fl(code * from) / to)), at most 127.  code * ratio differs
+// from that quotient by less than 127 * 4 * 2^-24 < 2^-14 (a rounding each in
+// 1 / to, ratio, the value and the quotient), so unless it lies within 2^-13 of a
+// half it rounds to the same integer; adding 1.5 * 2^23 rounds it and leaves the
+// integer in the low byte.  A value of the largest magnitude is 127 * to but for
+// its last bits and rounds to 127.  exact: take the division (a ratio that is
+// not finite; `to` may be denormal).
+__device__ __forceinline__ uint32_t requantise4(uint32_t word, float from, float to, float ratio, bool exact) {
+    constexpr float kHalf = 0.5f - 1.2207031e-04f;  // 1/2 - 2^-13
     const float2 magic = make_float2(12582912.f, 12582912.f), minus = make_float2(-12582912.f, -12582912.f);
-    float2 x[2];
-    code_floats(word, x[0], x[1]);
+    const float2 r2 = make_float2(ratio, ratio);
+    float2 c[2];
+    code_floats(word, c[0], c[1]);
     uint32_t out[2];
-    bool clear = true;
-    constexpr float kHalf = 0.5f - 6.1035156e-05f;  // 1/2 - 2^-14
+    float far = 0.f;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        x[i] = __fmul2_rn(x[i], make_float2(from, from));
-        const float2 q = __fmul2_rn(x[i], make_float2(inv, inv));
-        const float2 r = __fadd2_rn(q, magic);
-        const float2 t = __fadd2_rn(r, minus);
-        const float2 d = __fadd2_rn(q, make_float2(-t.x, -t.y));
-        clear = clear && fabsf(d.x) < kHalf && fabsf(d.y) < kHalf;
+        const float2 r = __ffma2_rn(c[i], r2, magic);
+        const float2 n = __fadd2_rn(r, minus);
+        const float2 d = __ffma2_rn(n, make_float2(-1.f, -1.f), __fmul2_rn(c[i], r2));
+        far = fmaxf(fmaxf(far, fabsf(d.x)), fabsf(d.y));
         out[i] = __byte_perm(__float_as_uint(r.x), __float_as_uint(r.y), 0x0040u);
     }
-    if (!clear) {  // near a half (or NaN: 1 / to overflowed): the division decides
-        return requantise_exact(x[0].x, to) | requantise_exact(x[0].y, to) << 8 | requantise_exact(x[1].x, to) << 16 |
-               requantise_exact(x[1].y, to) << 24;
+    if (far >= kHalf || exact) {
+        return requantise_exact(__fmul_rn(c[0].x, from), to) | requantise_exact(__fmul_rn(c[0].y, from), to) << 8 |
+               requantise_exact(__fmul_rn(c[1].x, from), to) << 16 | requantise_exact(__fmul_rn(c[1].y, from), to) << 24;
     }
     return __byte_perm(out[0], out[1], 0x5410u);
 }
@@ -524,7 +533,7 @@ __device__ __forceinline__ uint32_t requantise4(uint32_t word, float from, float
 // binary32 as in the quantised write (int8_write.cu).  Offsets kept[i] - i
 // never fall, so a block is untouched exactly when its last kept row stays.
 // A chunk is whole blocks; a warp's 16 rows lie in one block.
-__global__ void __launch_bounds__(kMoveThreads) evict_compact_i8_kernel(const CompactParams p) {
+__global__ void __launch_bounds__(kMoveThreads, 2) evict_compact_i8_kernel(const CompactParams p) {
     constexpr int RB = 128, LPR = 8, LOADS = kMoveRows * LPR / 32;
     __shared__ uint32_t s_max[3][kChunk / kMoveRows];  // three rounds: cleared a round ahead of its use
     pdl_wait();
@@ -600,9 +609,13 @@ __global__ void __launch_bounds__(kMoveThreads) evict_compact_i8_kernel(const Co
         if (base < n - stride) next = look(base + stride);
 #pragma unroll
         for (int u = 0; u < LOADS; ++u) {
-            const uint32_t m = max_codes(r[u].w, max_codes(r[u].z, max_codes(r[u].y, max_codes(r[u].x, 0u))));
+            uint32_t most = 0u, least = 0u;
+            range_codes(r[u].x, most, least);
+            range_codes(r[u].y, most, least);
+            range_codes(r[u].z, most, least);
+            range_codes(r[u].w, most, least);
             // |code| * |scale| rounds monotonically in |code|: the row's largest value
-            top = fmaxf(top, __fmul_rn((float)max(m & 0xFFFFu, m >> 16), fabsf(rs[u])));
+            top = fmaxf(top, __fmul_rn((float)largest_code(most, least), fabsf(rs[u])));
         }
         if (moved) {
 #pragma unroll
@@ -618,10 +631,12 @@ __global__ void __launch_bounds__(kMoveThreads) evict_compact_i8_kernel(const Co
                 const int from = u * (32 / LPR) + lane / LPR;
                 const int dst = __shfl_sync(0xffffffffu, m.dst, from);
                 if (scale > 0.f) {
-                    r[u].x = requantise4(r[u].x, rs[u], scale, inv);
-                    r[u].y = requantise4(r[u].y, rs[u], scale, inv);
-                    r[u].z = requantise4(r[u].z, rs[u], scale, inv);
-                    r[u].w = requantise4(r[u].w, rs[u], scale, inv);
+                    const float ratio = rs[u] * inv;
+                    const bool exact = !(fabsf(ratio) < 1024.f);  // more than 127 only where 1 / scale overflowed
+                    r[u].x = requantise4(r[u].x, rs[u], scale, ratio, exact);
+                    r[u].y = requantise4(r[u].y, rs[u], scale, ratio, exact);
+                    r[u].z = requantise4(r[u].z, rs[u], scale, ratio, exact);
+                    r[u].w = requantise4(r[u].w, rs[u], scale, ratio, exact);
                 } else {
                     r[u] = make_uint4(0u, 0u, 0u, 0u);
                 }
