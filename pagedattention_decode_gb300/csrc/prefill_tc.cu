@@ -265,8 +265,10 @@ __device__ __forceinline__ uint32_t code_pair<__nv_bfloat16>(uint32_t x, uint32_
 // rows of 64 dims: two 16-byte chunks.  The eight lanes of a store phase hold
 // one row; those of the second half of D write their odd chunk first, so the
 // phase covers eight distinct chunks of the banks.
+// sign: 1, or a factor of the values (-1 or 0, V codes only).
 template <typename T>
-__device__ __forceinline__ void store_codes(uint32_t tile, int half_bytes, int row, int col, const uint4 &v) {
+__device__ __forceinline__ void store_codes(uint32_t tile, int half_bytes, int row, int col, const uint4 &v,
+                                            float sign = 1.f) {
     uint4 lo, hi;
     lo.x = code_pair<T>(v.x, 0x4140u);
     lo.y = code_pair<T>(v.x, 0x4342u);
@@ -276,6 +278,14 @@ __device__ __forceinline__ void store_codes(uint32_t tile, int half_bytes, int r
     hi.y = code_pair<T>(v.z, 0x4342u);
     hi.z = code_pair<T>(v.w, 0x4140u);
     hi.w = code_pair<T>(v.w, 0x4342u);
+    if (sign != 1.f) {
+        uint32_t *w[8] = {&lo.x, &lo.y, &lo.z, &lo.w, &hi.x, &hi.y, &hi.z, &hi.w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float2 f = unpack2<T>(*w[i]);
+            *w[i] = pack2<T>(f.x * sign, f.y * sign);
+        }
+    }
     const bool odd = col >= 4;
     const uint32_t base = tile + (odd ? half_bytes : 0) + row * 128;
     const uint32_t c = (uint32_t)(col & 3) * 2, sw = (uint32_t)row & 7;
@@ -323,116 +333,115 @@ struct Regs {
 constexpr int kStageStride = 20;
 constexpr int kStageBytes = 2 * 4 * 32 * kStageStride * 4;
 
-// Two values as bf16 pairs hi + lo: hi their upper halves (one byte permutation;
-// rounding costs a conversion and buys nothing), lo the rest, rounded: off by
-// at most 2^-16 of the value.
-__device__ __forceinline__ void split_bf16(float a, float b, uint32_t &hi, uint32_t &lo) {
-    hi = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632u);
-    const float2 rest = __fadd2_rn(make_float2(a, b), make_float2(-__uint_as_float(__float_as_uint(a) & 0xFFFF0000u),
-                                                                  -__uint_as_float(__float_as_uint(b) & 0xFFFF0000u)));
-    lo = pack2<__nv_bfloat16>(rest.x, rest.y);
-}
+// What a step over an int8 cache needs of its eight 16-token sub-blocks.
+struct StepScales {
+    float k[8];    // K scale * softmax scale * log2 e
+    float lv[8];   // log2 |V scale|
+    float iv[8];   // 1 / |V scale|
+    float sign[8]; // -1, 0, 1: the factor of the V codes
+};
 
 // One step of a row's softmax over an int8 cache: 128 raw scores in TMEM become
-// P in their place (bf16, hi + lo).  Unlike the 16-bit step below, which holds
-// a whole row in registers, it walks 32 scores at a time, so that with a fourth
+// P in their place.  The V scale is folded into the exponent, P = 2^(score +
+// log2 vscale - M), so that P V needs only the codes: one fp16 P per key, as
+// over a 16-bit fp16 cache (11 significant bits, relative error <= 2^-11, where
+// the codes themselves are off by up to half of 1/127 of their block's largest),
+// with M a running maximum of score + log2 vscale; the row's sum takes each
+// sub-block's P back by 1 / vscale.  M moves when a key passes it by more than
+// 15 (P <= 2^15): then O and the sum are scaled down.
+// Unlike the 16-bit step below, which holds a whole row in registers, this one
+// walks 32 scores at a time, twice (the maximum, then P), so that with a fourth
 // warpgroup every thread fits the 128 registers of a 512-thread launch (a whole
-// row spilled 664 bytes), and in a loop that is not unrolled: beside the
+// row spilled 664 bytes), and in loops that are not unrolled: beside the
 // converting warps' code the instruction cache is what runs out (chunks of the
-// mixed step, 16 x 512 rows over 2,560 keys, us: four parts unrolled 519, two 421,
-// one 404, though its TMEM loads are not overlapped).  `scl`: 8 factors of the scores (K scale,
-// softmax scale, log2 e), 8 V scales.  hi_c, lo_c: the row sees the step's keys
-// lo_c .. hi_c.
-// The running maximum moves when a score passes it by more than 15 (p <= 2^15):
-// then O, the sum and what the step has already written of P are scaled down.
-// (Letting the sum of 32 p tell instead, as the 16-bit step does, needs no
-// maximum but makes the next part wait for the vote: 460 -> 507 us then.)
+// mixed step, 16 x 512 rows over 2,560 keys, with P as a bf16 hi + lo pair and the
+// V scale multiplied in, us: four parts unrolled 519, two 421, one 404).
+// hi_c, lo_c: the row sees the step's keys lo_c .. hi_c.
 template <int D>
-__device__ __forceinline__ void softmax_step_i8(uint32_t trow, const float *scl, bool whole, int hi_c, int lo_c,
+__device__ __forceinline__ void softmax_step_i8(uint32_t trow, const StepScales &scl, bool whole, int hi_c, int lo_c,
                                                 bool has_o, float &m_used, float &lsum) {
     constexpr float kLead = 15.f;
-    float2 sum = make_float2(0.f, 0.f);
+    float most = -INFINITY;
 #pragma unroll 1
     for (int cc = 0; cc < kTok / 32; ++cc) {
         uint32_t sr[32];
         tmem_ld32(trow + 32 * cc, sr);
         tmem_wait_ld();
-        const float2 ks = *reinterpret_cast<const float2 *>(scl + 2 * cc);
-        const float2 vs = *reinterpret_cast<const float2 *>(scl + 8 + 2 * cc);
+        const float2 ks = *reinterpret_cast<const float2 *>(&scl.k[2 * cc]);
+        const float2 lv = *reinterpret_cast<const float2 *>(&scl.lv[2 * cc]);
+        if (whole && ks.x >= 0.f && ks.y >= 0.f) {
+            float top[4];
 #pragma unroll
-        for (int c = 0; c < 32; c += 2) {
-            const float k = c < 16 ? ks.x : ks.y;
-            const float2 x =
-                __fmul2_rn(make_float2(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), make_float2(k, k));
-            sr[c] = __float_as_uint(x.x);
-            sr[c + 1] = __float_as_uint(x.y);
-        }
-        if (!whole) {  // masked after the factor: a scale of 0 would turn a masked -inf into NaN
+            for (int v = 0; v < 4; ++v)
+                top[v] = fmax3(__uint_as_float(sr[8 * v]), __uint_as_float(sr[8 * v + 1]),
+                               fmax3(__uint_as_float(sr[8 * v + 2]), __uint_as_float(sr[8 * v + 3]),
+                                     fmax3(__uint_as_float(sr[8 * v + 4]), __uint_as_float(sr[8 * v + 5]),
+                                           fmaxf(__uint_as_float(sr[8 * v + 6]), __uint_as_float(sr[8 * v + 7])))));
+            most = fmax3(most, fmaf(fmaxf(top[0], top[1]), ks.x, lv.x), fmaf(fmaxf(top[2], top[3]), ks.y, lv.y));
+        } else {
 #pragma unroll
             for (int c = 0; c < 32; ++c)
-                if (32 * cc + c > hi_c || 32 * cc + c < lo_c) sr[c] = __float_as_uint(-INFINITY);
+                if (32 * cc + c <= hi_c && 32 * cc + c >= lo_c)
+                    most = fmaxf(most, fmaf(__uint_as_float(sr[c]), c < 16 ? ks.x : ks.y, c < 16 ? lv.x : lv.y));
         }
-        float top[4];
-#pragma unroll
-        for (int v = 0; v < 4; ++v)
-            top[v] = fmax3(__uint_as_float(sr[8 * v]), __uint_as_float(sr[8 * v + 1]),
-                           fmax3(__uint_as_float(sr[8 * v + 2]), __uint_as_float(sr[8 * v + 3]),
-                                 fmax3(__uint_as_float(sr[8 * v + 4]), __uint_as_float(sr[8 * v + 5]),
-                                       fmaxf(__uint_as_float(sr[8 * v + 6]), __uint_as_float(sr[8 * v + 7])))));
-        const float most = fmaxf(fmax3(top[0], top[1], top[2]), top[3]);
-        const bool over = most > m_used + kLead || (m_used == -INFINITY && most > -INFINITY);
-        if (__any_sync(0xffffffffu, over)) {
-            const float m_new = over ? fmaxf(m_used, most) : m_used;
-            const float alpha = over ? fast_exp2(m_used - m_new) : 1.f;
-            m_used = m_new;
-            lsum *= alpha;
-            sum.x *= alpha;
-            sum.y *= alpha;
-            if (cc > 0) tmem_wait_st();  // the earlier parts of P have been written
+    }
+    const bool over = most > m_used + kLead || (m_used == -INFINITY && most > -INFINITY);
+    if (__any_sync(0xffffffffu, over)) {
+        const float m_new = over ? most : m_used;
+        const float alpha = over ? fast_exp2(m_used - m_new) : 1.f;
+        m_used = m_new;
+        lsum *= alpha;
+        if (has_o) {
 #pragma unroll 1
-            for (int i8 = 0; i8 < 2 * cc; ++i8) {  // 16 keys: eight columns of hi, eight of lo
-                const uint32_t c0 = (uint32_t)(i8 >> 1) * 32u + (uint32_t)(i8 & 1) * 8u;
-                uint32_t h[8], l[8];
-                tmem_ld8(trow + c0, h);
-                tmem_ld8(trow + c0 + 16, l);
+            for (int c0 = 0; c0 < D; c0 += 8) {
+                uint32_t o[8];
+                tmem_ld8(trow + 128 + c0, o);
                 tmem_wait_ld();
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float2 a = unpack2<__nv_bfloat16>(h[i]), b = unpack2<__nv_bfloat16>(l[i]);
-                    split_bf16((a.x + b.x) * alpha, (a.y + b.y) * alpha, h[i], l[i]);
-                }
-                tmem_st8(trow + c0, h);
-                tmem_st8(trow + c0 + 16, l);
-            }
-            if (has_o) {
-#pragma unroll 1
-                for (int c0 = 0; c0 < D; c0 += 8) {
-                    uint32_t o[8];
-                    tmem_ld8(trow + 128 + c0, o);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-                    tmem_st8(trow + 128 + c0, o);
-                }
+                for (int i = 0; i < 8; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                tmem_st8(trow + 128 + c0, o);
             }
         }
-        // a row that has met no key yet: every score and m_used are -inf, p = 0
-        const float neg_m = m_used == -INFINITY ? -INFINITY : -m_used;
-        uint32_t ph[16], pl[16];
-#pragma unroll
-        for (int c = 0; c < 32; c += 2) {
-            const float v = c < 16 ? vs.x : vs.y;
-            const float2 x = __fadd2_rn(make_float2(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])),
-                                        make_float2(neg_m, neg_m));
-            const float2 pr = make_float2(fast_exp2(x.x), fast_exp2(x.y));
-            sum = __fadd2_rn(sum, pr);
-            const float2 pv = __fmul2_rn(pr, make_float2(v, v));
-            split_bf16(pv.x, pv.y, ph[c / 2], pl[c / 2]);
-        }
-        tmem_st16(trow + 32 * cc, ph);
-        tmem_st16(trow + 32 * cc + 16, pl);
     }
-    lsum += sum.x + sum.y;
+    // a row that has met no key yet: every score and m_used are -inf, P = 0
+    const float neg_m = m_used == -INFINITY ? -INFINITY : -m_used;
+#pragma unroll 1
+    for (int cc = 0; cc < kTok / 32; ++cc) {
+        uint32_t sr[32], ph[16];
+        tmem_ld32(trow + 32 * cc, sr);
+        tmem_wait_ld();
+        const float2 ks = *reinterpret_cast<const float2 *>(&scl.k[2 * cc]);
+        const float2 lv = *reinterpret_cast<const float2 *>(&scl.lv[2 * cc]);
+        const float2 iv = *reinterpret_cast<const float2 *>(&scl.iv[2 * cc]);
+        if (!whole) {  // (a factor of 0 would turn a masked -inf into NaN: the mask comes after it)
+#pragma unroll
+            for (int c = 0; c < 32; ++c) {
+                const float x = fmaf(__uint_as_float(sr[c]), c < 16 ? ks.x : ks.y, (c < 16 ? lv.x : lv.y) + neg_m);
+                sr[c] = __float_as_uint(32 * cc + c > hi_c || 32 * cc + c < lo_c ? -INFINITY : x);
+            }
+        } else {
+#pragma unroll
+            for (int c = 0; c < 32; c += 2) {
+                const float k = c < 16 ? ks.x : ks.y, add = (c < 16 ? lv.x : lv.y) + neg_m;
+                const float2 x = __ffma2_rn(make_float2(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])),
+                                            make_float2(k, k), make_float2(add, add));
+                sr[c] = __float_as_uint(x.x);
+                sr[c + 1] = __float_as_uint(x.y);
+            }
+        }
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int c = 16 * b; c < 16 * b + 16; c += 2) {
+                const float2 pr = make_float2(fast_exp2(__uint_as_float(sr[c])), fast_exp2(__uint_as_float(sr[c + 1])));
+                sum = __fadd2_rn(sum, pr);
+                ph[c / 2] = pack2<__half>(pr.x, pr.y);
+            }
+            lsum = fmaf(sum.x + sum.y, b ? iv.y : iv.x, lsum);
+        }
+        tmem_st16(trow + 16 * cc, ph);
+    }
 }
 
 // A work item: the pair of q tiles `pair` (2 x 128 M rows) of KV head `kvh`
@@ -445,11 +454,10 @@ struct TcItem {
 
 // I8: the pools hold int8 codes with a scale per block and KV head.  The
 // products run on the codes, which are exact as 16-bit values: K in the query's
-// type, V in bf16.  The producer stages the codes (TMA) and leaves the tile's
+// type, V in fp16.  The producer stages the codes (TMA) and leaves the tile's
 // 8 + 8 scales in a ring of their own; warps 12-15 convert the codes in
-// registers and write the swizzled tiles that TMA writes otherwise.  The softmax warps multiply the scores by their block's K scale
-// in binary32 and the weights by its V scale before they are split into a
-// bf16 hi + lo pair, whose exponent range holds any scale.
+// registers and write the swizzled tiles that TMA writes otherwise.  The softmax
+// warps apply the scales (softmax_step_i8).
 template <int D, typename T, bool I8 = false>
 __global__ void __launch_bounds__(Regs<I8>::kThreads, 1)
     prefill_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
@@ -463,23 +471,21 @@ __global__ void __launch_bounds__(Regs<I8>::kThreads, 1)
     constexpr int KVHALF = kTok * 128;           // bytes of 128 tokens x 64 dims
     constexpr int KVSTAGE = HALVES * KVHALF;     // one K (or V) tile
     constexpr bool BF = IsBf16<T>::value;
-    using TP = std::conditional_t<I8, __nv_bfloat16, T>;  // the type of P and V in P V
     // P enters P V as a 16-bit operand.  fp16 keeps 11 significant bits of each
     // p in [0, 2^15] (relative error <= 2^-12, far inside the 2e-3 gate); bf16
     // keeps only 8, so there P is split into hi + lo halves and P V takes two
     // MMAs per K step.  P of keys 32c .. 32c + 31 lies in TMEM columns
     // 16c .. 16c + 15 (fp16), or hi in 32c .. 32c + 15 and lo in 32c + 16 ..
     // 32c + 31 (bf16): columns whose scores have already been read.
-    constexpr bool LO = BF || I8;
+    constexpr bool LO = BF && !I8;
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t bars[2 + 4 * S + 3 * kTiles + 4 + 1 + (I8 ? 4 : 0)];
     __shared__ TcItem s_item[2];
     __shared__ uint32_t s_tmem;
     __shared__ volatile int s_abort;
-    // int8: scale * log2(e) * K scale and V scale of the 16-token sub-blocks of a
-    // step, slot = step % 4.  The fill of step g + 4 follows the release of step
+    // int8: the scales of the 16-token sub-blocks of a step, slot = step % 4.  The fill of step g + 4 follows the release of step
     // g + 3's K, whose score MMAs follow the softmax of step g + 2.
-    __shared__ __align__(16) float s_scales[I8 ? 4 : 1][16];
+    __shared__ __align__(16) StepScales s_scales[I8 ? 4 : 1];
     uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t *sq = base;
     uint8_t *sk = base + kTiles * QTILE;
@@ -753,6 +759,10 @@ __global__ void __launch_bounds__(Regs<I8>::kThreads, 1)
                         ks = p.k_scale[at] * p.scale_log2;
                         vs = p.v_scale[at];
                     }
+                    // a V scale too small for 1 / scale (0 among them: values under 2^-93) counts as 0:
+                    // its codes are multiplied by 0, its P by a scale of 1
+                    const bool zero = fabsf(vs) < 7.8886091e-31f;  // 2^-100
+                    const float lv = zero ? 0.f : log2f(fabsf(vs)), iv = zero ? 1.f : 1.f / fabsf(vs);
                     lookup(j + 1);
                     const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, mine)) * box * 128;
 #pragma unroll
@@ -764,8 +774,11 @@ __global__ void __launch_bounds__(Regs<I8>::kThreads, 1)
                             break;
                         }
                         if (which == 0 && lane < 8) {
-                            s_scales[I8 ? gs & 3 : 0][lane] = ks;
-                            s_scales[I8 ? gs & 3 : 0][8 + lane] = vs;
+                            StepScales &scl = s_scales[I8 ? gs & 3 : 0];
+                            scl.k[lane] = ks;
+                            scl.lv[lane] = lv;
+                            scl.iv[lane] = iv;
+                            scl.sign[lane] = zero ? 0.f : copysignf(1.f, vs);
                         }
                         __syncwarp();
                         if (lane == 0) mbar_arrive_expect_tx(&code_full[which], bytes);
@@ -805,7 +818,7 @@ __global__ void __launch_bounds__(Regs<I8>::kThreads, 1)
             return __all_sync(0xffffffffu, wait_phase(bar, parity, &s_abort));
         };
         const uint32_t idS = idesc_f16(BF ? 1 : 0, 0, 128, kTok);
-        const uint32_t idPV = idesc_f16(BF || I8 ? 1 : 0, 1, 128, D);
+        const uint32_t idPV = idesc_f16(BF && !I8 ? 1 : 0, 1, 128, D);
         const uint32_t sq_a = smem_u32(sq), sk_a = smem_u32(sk), sv_a = smem_u32(sv);
         // g: ring position of the K / V step
         auto issue_s = [&](int u, int g) {
@@ -944,7 +957,9 @@ __global__ void __launch_bounds__(Regs<I8>::kThreads, 1)
                 if (!ok) break;
 #pragma unroll 1
                 for (int i = 0; i < SUBS; ++i)
-                    store_codes<TP>(sv_a + (gs % S) * KVSTAGE, KVHALF, i * 16 + r16, col, ld_shared_u4(codes + kCodeBytes / 2 + i * 2048));
+                    store_codes<__half>(sv_a + (gs % S) * KVSTAGE, KVHALF, i * 16 + r16, col,
+                                        ld_shared_u4(codes + kCodeBytes / 2 + i * 2048),
+                                        s_scales[I8 ? gs & 3 : 0].sign[i]);
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
                 if (lane == 0) {

@@ -36,10 +36,12 @@ def _case(seed, q_lens, kv_lens, hq, hkv, bs, dtype, k_size=0.02, v_size=0.02):
 
 def _reference(q, kq, vq, ks, vs, tab, cu, lens, scale, causal=True, window=0, skip=()):
     """Binary64 outputs and the bound on a row's error: a weight's relative error (scores: sums of 128 products that
-    truncate and two scalings, as in the key-weight tests; exp2 and the row sum) plus 2^-16 of the hi + lo split and
-    2^-24 per key of the accumulation, times sum p |v|; decode rows are held to the decode call's tolerance.  Below
-    binary32's (and bf16's) normal range nothing is relative: a weight (sum of weights >= 1, as the maximum's is 1) or
-    a weight times its V scale under 2^-126 is off by at most that, for each of L keys and times a code of at most 128."""
+    truncate and two scalings, as in the key-weight tests; exp2 and the row sum) plus half a step of fp16, 2^-11, for a
+    chunk's weights and 2^-24 per key of the accumulation, times sum p |v|; decode rows are held to the decode call's
+    tolerance.  Below fp16's normal range a weight is off by 2^-25 at most: weights are p times the V scale in units of
+    the largest of them, so a key's error is at most 2^-25 of the largest V scale times a code of at most 128; the
+    folded log2 of a scale (off by 2^-24 of at most 128) is 2^-17 of each weight.  A row whose weights are all under
+    2^-126 apart from the largest loses them: L 2^-126 times 128 codes."""
     bs, hkv = kq.shape[1], kq.shape[2]
     hq = q.shape[1]
     g = hq // hkv
@@ -66,8 +68,8 @@ def _reference(q, kq, vq, ks, vs, tab, cu, lens, scale, causal=True, window=0, s
             p = e / e.sum(1, keepdims=True)
             want[a:b, h] = p @ v[:, h // g]
             mag = abs(scale) * (np.abs(qd[a:b, h]) @ np.abs(k[:, h // g]).T)[seen].max()
-            rel = math.expm1(2 * 130 * 2.0 ** -23 * mag) + 2.0 ** -16 + (L + 4) * 2.0 ** -24
-            tiny = L * 2.0 ** -126 * 128 * (1 + vs[blk, h // g].max())
+            rel = math.expm1(2 * 130 * 2.0 ** -23 * mag) + (2.0 ** -11 + 2.0 ** -17 if n > 1 else 2.0 ** -16) + (L + 4) * 2.0 ** -24
+            tiny = L * 128 * (2.0 ** -126 + 2.0 ** -25 * float(vs[blk, h // g].max()))
             bound[a:b, h] = rel * (p @ np.abs(v[:, h // g])) + tiny + (TOL if n == 1 else 0)
     return want, bound
 
@@ -145,6 +147,24 @@ def test_zero_blocks_and_values_that_are_not_seen():
     out = _run(case, 128 ** -0.5, err=err, window=100)
     clean = (q, kq, vq, np.nan_to_num(ks), np.nan_to_num(vs), tab, cu, lens)
     want, bound = _reference(*clean, 128 ** -0.5, window=100)
+    assert int(err) == 0 and (np.abs(out.cpu().double().numpy() - want) <= bound).all()
+
+
+def test_scales_of_any_sign_and_zero_over_codes():
+    """Scales are plain factors: negative ones, zeros over codes that are not zero, and V scales from 1e-3 to 10 in one row."""
+    case = _case(41, [150, 3], [600, 333], 16, 4, 16, "f16")
+    r = np.random.default_rng(5)
+    for sc in (case[3], case[4]):
+        sc[r.random(sc.shape) < 0.2] *= -1
+        sc[r.random(sc.shape) < 0.1] = 0
+    case[4][r.random(case[4].shape) < 0.3] *= 500
+    case[4][r.random(case[4].shape) < 0.3] *= 0.05
+    q, kq, vq, ks, vs, tab, cu, lens = case
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = _run(case, 128 ** -0.5, err=err)
+    want, bound = _reference(*case, 128 ** -0.5)
+    # the bound's largest V scale counts by magnitude
+    bound += lens.max() * 128 * 2.0 ** -25 * np.nanmax(np.abs(vs))
     assert int(err) == 0 and (np.abs(out.cpu().double().numpy() - want) <= bound).all()
 
 
