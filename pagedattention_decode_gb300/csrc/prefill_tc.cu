@@ -347,48 +347,33 @@ struct StepScales {
 // over a 16-bit fp16 cache (11 significant bits, relative error <= 2^-11, where
 // the codes themselves are off by up to half of 1/127 of their block's largest),
 // with M a running maximum of score + log2 vscale; the row's sum takes each
-// sub-block's P back by 1 / vscale.  M moves when a key passes it by more than
-// 15 (P <= 2^15): then O and the sum are scaled down.
-// Unlike the 16-bit step below, which holds a whole row in registers, this one
-// walks 32 scores at a time, twice (the maximum, then P), so that with a fourth
-// warpgroup every thread fits the 128 registers of a 512-thread launch (a whole
-// row spilled 664 bytes), and in loops that are not unrolled: beside the
-// converting warps' code the instruction cache is what runs out (chunks of the
-// mixed step, 16 x 512 rows over 2,560 keys, with P as a bf16 hi + lo pair and the
-// V scale multiplied in, us: four parts unrolled 519, two 421, one 404).
+// sub-block's P back by 1 / vscale.
+// Unlike the 16-bit step below, which holds a row's scores in registers, this
+// one reads 32 at a time and holds P (64 registers), so that with a fourth
+// warpgroup every thread fits the 128 registers of a 512-thread launch (a row
+// of scores spilled 664 bytes).  The scores stay in TMEM until the step's P sum
+// to at most 2^15, which proves every P finite as fp16: M comes from the row's
+// first visible keys and is taken again, O and the sum scaled down and P
+// computed once more, only where they do not.
 // hi_c, lo_c: the row sees the step's keys lo_c .. hi_c.
 template <int D>
 __device__ __forceinline__ void softmax_step_i8(uint32_t trow, const StepScales &scl, bool whole, int hi_c, int lo_c,
                                                 bool has_o, float &m_used, float &lsum) {
-    constexpr float kLead = 15.f;
-    float most = -INFINITY;
+    // M becomes the largest of the step's visible keys on the lanes that ask
+    auto raise = [&](bool ask) {
+        float most = -INFINITY;
 #pragma unroll 1
-    for (int cc = 0; cc < kTok / 32; ++cc) {
-        uint32_t sr[32];
-        tmem_ld32(trow + 32 * cc, sr);
-        tmem_wait_ld();
-        const float2 ks = *reinterpret_cast<const float2 *>(&scl.k[2 * cc]);
-        const float2 lv = *reinterpret_cast<const float2 *>(&scl.lv[2 * cc]);
-        if (whole && ks.x >= 0.f && ks.y >= 0.f) {
-            float top[4];
+        for (int cc = 0; cc < kTok / 8; ++cc) {
+            uint32_t sr[8];
+            tmem_ld8(trow + 8 * cc, sr);
+            tmem_wait_ld();
 #pragma unroll
-            for (int v = 0; v < 4; ++v)
-                top[v] = fmax3(__uint_as_float(sr[8 * v]), __uint_as_float(sr[8 * v + 1]),
-                               fmax3(__uint_as_float(sr[8 * v + 2]), __uint_as_float(sr[8 * v + 3]),
-                                     fmax3(__uint_as_float(sr[8 * v + 4]), __uint_as_float(sr[8 * v + 5]),
-                                           fmaxf(__uint_as_float(sr[8 * v + 6]), __uint_as_float(sr[8 * v + 7])))));
-            most = fmax3(most, fmaf(fmaxf(top[0], top[1]), ks.x, lv.x), fmaf(fmaxf(top[2], top[3]), ks.y, lv.y));
-        } else {
-#pragma unroll
-            for (int c = 0; c < 32; ++c)
-                if (32 * cc + c <= hi_c && 32 * cc + c >= lo_c)
-                    most = fmaxf(most, fmaf(__uint_as_float(sr[c]), c < 16 ? ks.x : ks.y, c < 16 ? lv.x : lv.y));
+            for (int c = 0; c < 8; ++c)
+                if (8 * cc + c <= hi_c && 8 * cc + c >= lo_c)
+                    most = fmaxf(most, fmaf(__uint_as_float(sr[c]), scl.k[cc >> 1], scl.lv[cc >> 1]));
         }
-    }
-    const bool over = most > m_used + kLead || (m_used == -INFINITY && most > -INFINITY);
-    if (__any_sync(0xffffffffu, over)) {
-        const float m_new = over ? most : m_used;
-        const float alpha = over ? fast_exp2(m_used - m_new) : 1.f;
+        const float m_new = ask ? fmaxf(m_used, most) : m_used;
+        const float alpha = m_new > m_used ? fast_exp2(m_used - m_new) : 1.f;
         m_used = m_new;
         lsum *= alpha;
         if (has_o) {
@@ -401,25 +386,27 @@ __device__ __forceinline__ void softmax_step_i8(uint32_t trow, const StepScales 
                 for (int i = 0; i < 8; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
                 tmem_st8(trow + 128 + c0, o);
             }
+            tmem_wait_st();
         }
-    }
-    // a row that has met no key yet: every score and m_used are -inf, P = 0
-    const float neg_m = m_used == -INFINITY ? -INFINITY : -m_used;
+    };
+    const bool fresh = m_used == -INFINITY && hi_c >= 0 && lo_c < kTok;
+    if (__any_sync(0xffffffffu, fresh)) raise(fresh);
+    uint32_t ph[kTok / 2];
+    float step_sum;
 #pragma unroll 1
-    for (int cc = 0; cc < kTok / 32; ++cc) {
-        uint32_t sr[32], ph[16];
-        tmem_ld32(trow + 32 * cc, sr);
-        tmem_wait_ld();
-        const float2 ks = *reinterpret_cast<const float2 *>(&scl.k[2 * cc]);
-        const float2 lv = *reinterpret_cast<const float2 *>(&scl.lv[2 * cc]);
-        const float2 iv = *reinterpret_cast<const float2 *>(&scl.iv[2 * cc]);
-        if (!whole) {  // (a factor of 0 would turn a masked -inf into NaN: the mask comes after it)
+    for (int pass = 0;; ++pass) {
+        // a row that has met no key yet: every score and m_used are -inf, P = 0
+        const float neg_m = m_used == -INFINITY ? -INFINITY : -m_used;
+        float total = 0.f;
+        step_sum = 0.f;
 #pragma unroll
-            for (int c = 0; c < 32; ++c) {
-                const float x = fmaf(__uint_as_float(sr[c]), c < 16 ? ks.x : ks.y, (c < 16 ? lv.x : lv.y) + neg_m);
-                sr[c] = __float_as_uint(32 * cc + c > hi_c || 32 * cc + c < lo_c ? -INFINITY : x);
-            }
-        } else {
+        for (int cc = 0; cc < kTok / 32; ++cc) {
+            uint32_t sr[32];
+            tmem_ld32(trow + 32 * cc, sr);
+            tmem_wait_ld();
+            const float2 ks = *reinterpret_cast<const float2 *>(&scl.k[2 * cc]);
+            const float2 lv = *reinterpret_cast<const float2 *>(&scl.lv[2 * cc]);
+            const float2 iv = *reinterpret_cast<const float2 *>(&scl.iv[2 * cc]);
 #pragma unroll
             for (int c = 0; c < 32; c += 2) {
                 const float k = c < 16 ? ks.x : ks.y, add = (c < 16 ? lv.x : lv.y) + neg_m;
@@ -428,20 +415,32 @@ __device__ __forceinline__ void softmax_step_i8(uint32_t trow, const StepScales 
                 sr[c] = __float_as_uint(x.x);
                 sr[c + 1] = __float_as_uint(x.y);
             }
-        }
+            if (!whole) {
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-            float2 sum = make_float2(0.f, 0.f);
-#pragma unroll
-            for (int c = 16 * b; c < 16 * b + 16; c += 2) {
-                const float2 pr = make_float2(fast_exp2(__uint_as_float(sr[c])), fast_exp2(__uint_as_float(sr[c + 1])));
-                sum = __fadd2_rn(sum, pr);
-                ph[c / 2] = pack2<__half>(pr.x, pr.y);
+                for (int c = 0; c < 32; ++c)
+                    if (32 * cc + c > hi_c || 32 * cc + c < lo_c) sr[c] = __float_as_uint(-INFINITY);
             }
-            lsum = fmaf(sum.x + sum.y, b ? iv.y : iv.x, lsum);
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int c = 16 * b; c < 16 * b + 16; c += 2) {
+                    const float2 pr = make_float2(fast_exp2(__uint_as_float(sr[c])), fast_exp2(__uint_as_float(sr[c + 1])));
+                    sum = __fadd2_rn(sum, pr);
+                    ph[16 * cc + c / 2] = pack2<__half>(pr.x, pr.y);
+                }
+                const float both = sum.x + sum.y;
+                total += both;
+                step_sum = fmaf(both, b ? iv.y : iv.x, step_sum);
+            }
         }
-        tmem_st16(trow + 16 * cc, ph);
+        const bool over = pass == 0 && !(total <= kPSumMax);
+        if (!__any_sync(0xffffffffu, over)) break;
+        raise(over);
     }
+    lsum += step_sum;
+    tmem_st32(trow, *reinterpret_cast<uint32_t(*)[32]>(&ph[0]));
+    tmem_st32(trow + 32, *reinterpret_cast<uint32_t(*)[32]>(&ph[32]));
 }
 
 // A work item: the pair of q tiles `pair` (2 x 128 M rows) of KV head `kvh`
