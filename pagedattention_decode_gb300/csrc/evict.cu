@@ -529,8 +529,9 @@ __device__ __forceinline__ uint32_t requantise4(uint32_t word, float from, float
 }
 
 // The int8 cache: a block in which some row of the head moves gets a new
-// scale, max|x| / 127 over its kept rows, and new codes, every decision in
-// binary32 as in the quantised write (int8_write.cu).  Offsets kept[i] - i
+// scale, max|x| times binary32's 1/127 over its kept rows (an ulp at most from the
+// quotient that the quantised write takes), and new codes, every decision in
+// binary32 as there.  Offsets kept[i] - i
 // never fall, so a block is untouched exactly when its last kept row stays.
 // A chunk is whole blocks; a warp's 16 rows lie in one block.
 __global__ void __launch_bounds__(kMoveThreads, 2) evict_compact_i8_kernel(const CompactParams p) {
@@ -624,7 +625,7 @@ __global__ void __launch_bounds__(kMoveThreads, 2) evict_compact_i8_kernel(const
         }
         unit_sync(p.cluster);  // every source of the round is read, every block's maximum known
         if (moved) {
-            const float scale = __fdiv_rn(__uint_as_float(s_max[round][slot]), 127.f);
+            const float scale = __fmul_rn(__uint_as_float(s_max[round][slot]), 1.f / 127.f);
             const float inv = __fdiv_rn(1.f, scale);
 #pragma unroll
             for (int u = 0; u < LOADS; ++u) {

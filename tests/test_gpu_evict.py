@@ -150,7 +150,7 @@ def _compact(pools, scales, w, tables, lens, kept, budget):
                     sel = dst // bs == b
                     if np.array_equal(src[sel], dst[sel]):
                         continue
-                    scale = np.float32(np.abs(vals[sel]).max()) / np.float32(127)
+                    scale = np.float32(np.abs(vals[sel]).max()) * (np.float32(1) / np.float32(127))
                     q = np.clip(np.rint(vals[sel] / scale), -127, 127) if scale > 0 else np.zeros_like(vals[sel])
                     x[tab[b], dst[sel] % bs, h] = q.astype(np.int8)
                     sc[tab[b], h] = scale
