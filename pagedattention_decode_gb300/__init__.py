@@ -76,9 +76,10 @@ def _cache(k_cache: torch.Tensor, v_cache: torch.Tensor) -> PkvCache:
 
 def _row_stride(t: torch.Tensor, name: str) -> int:
     """Elements between rows of a [rows, heads, dim] tensor with heads/dims packed."""
-    if t.dim() != 3 or t.stride(2) != 1 or t.stride(1) != t.shape[2]:
+    st = t.stride()
+    if len(st) != 3 or st[2] != 1 or st[1] != t.shape[2]:
         raise ValueError(f"{name} must be [rows, heads, head_dim] with heads and dims contiguous")
-    return t.stride(0)
+    return st[0]
 
 
 def _check_i32(t: torch.Tensor, name: str) -> None:
@@ -104,11 +105,12 @@ def write_kv(k: torch.Tensor, v: torch.Tensor, slot_mapping: torch.Tensor, k_cac
                              ctypes.byref(c), _ptr(err), _stream(stream)))
 
 
-def _on_current_device(**tensors: Optional[torch.Tensor]) -> None:
+def _on_current_device(names: str, *tensors: Optional[torch.Tensor]) -> None:
     """Every given tensor lies on the current CUDA device (where the call's stream is)."""
     dev = torch.cuda.current_device()
-    for name, t in tensors.items():
+    for i, t in enumerate(tensors):
         if t is not None and (not isinstance(t, torch.Tensor) or t.get_device() != dev):
+            name = names.split()[i]
             _cuda(t, name)
             raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
 
@@ -118,18 +120,22 @@ def _check_err(err: Optional[torch.Tensor]) -> None:
         raise TypeError("err must be an int32 CUDA tensor")
 
 
-def _key_weights(w: torch.Tensor, num_seqs: int, num_kv_heads: int, keys: int, name: str = "key_weights"):
+def _key_weights(w: torch.Tensor, num_seqs: int, num_kv_heads: int, keys: int):
     """The strides of accumulated weights [B, Hkv, >= keys] float32, keys contiguous."""
     if w.dtype != torch.float32 or w.dim() != 3:
-        raise TypeError(f"{name} must be float32 [num_seqs, num_kv_heads, max_keys]")
-    if w.shape[0] != num_seqs or w.shape[1] != num_kv_heads or w.shape[2] < keys:
-        raise ValueError(f"{name} must be [{num_seqs}, {num_kv_heads}, {keys} or more] for these tables, "
+        raise TypeError("key_weights must be float32 [num_seqs, num_kv_heads, max_keys]")
+    B, hkv, cap = w.shape
+    if B != num_seqs or hkv != num_kv_heads or cap < keys:
+        raise ValueError(f"key_weights must be [{num_seqs}, {num_kv_heads}, {keys} or more] for these tables, "
                          f"got {list(w.shape)}")
-    if w.shape[2] > 1 and w.stride(2) != 1:
-        raise ValueError(f"{name}: the keys of a head must be contiguous")
+    seq, head, key = w.stride()
+    if cap > 1 and key != 1:
+        raise ValueError("key_weights: the keys of a head must be contiguous")
     # strides of dimensions of length 1 are never used: any value that does not overlap
-    head = w.stride(1) if num_kv_heads > 1 else w.shape[2]
-    seq = w.stride(0) if num_seqs > 1 else max(0, num_kv_heads - 1) * head + w.shape[2]
+    if hkv <= 1:
+        head = cap
+    if B <= 1:
+        seq = max(0, hkv - 1) * head + cap
     return seq, head
 
 
@@ -231,8 +237,8 @@ def attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, b
 def _decode_weights(call: str, c, q, block_tables, seq_lens, scale, window, key_weights, out, workspace, err, stream):
     """The decode calls that accumulate key weights (16-bit and int8 caches); out is allocated."""
     B, hq, d = q.shape
-    _on_current_device(q=q, block_tables=block_tables, seq_lens=seq_lens, key_weights=key_weights, out=out,
-                       workspace=workspace, err=err)
+    _on_current_device("q block_tables seq_lens key_weights out workspace err", q, block_tables, seq_lens, key_weights,
+                       out, workspace, err)
     _check_err(err)
     _same_rows(B, block_tables, seq_lens)
     if out.dtype not in _DT or not out.is_contiguous() or out.shape != q.shape:
@@ -352,8 +358,8 @@ def attn_varlen_int8(q: torch.Tensor, kq: torch.Tensor, vq: torch.Tensor, k_scal
     """:func:`attn_varlen` over an int8 cache: packed rows q fp16/bf16 [total_q, Hq, D],
     cu_seqlens_q [B+1], seq_lens = kv_len [B], the new rows' keys already written."""
     c = _cache_i8(kq, vq, k_scale, v_scale, q.dtype)
-    _on_current_device(q=q, kq=kq, vq=vq, k_scale=k_scale, v_scale=v_scale, block_tables=block_tables,
-                       cu_seqlens_q=cu_seqlens_q, seq_lens=seq_lens, out=out, workspace=workspace, err=err)
+    _on_current_device("q kq vq k_scale v_scale block_tables cu_seqlens_q seq_lens out workspace err", q, kq, vq, k_scale,
+                       v_scale, block_tables, cu_seqlens_q, seq_lens, out, workspace, err)
     _check_err(err)
     for t, n in ((block_tables, "block_tables"), (seq_lens, "seq_lens"), (cu_seqlens_q, "cu_seqlens_q")):
         _check_i32(t, n)
@@ -386,7 +392,7 @@ def evict_select(key_weights: torch.Tensor, seq_lens: torch.Tensor, budget: int,
     positions and, in each head, those of largest weight besides (ties: the
     lowest position).  Returns kept [B, Hkv, budget] int32 (ascending, then -1)
     and new_lens [B] int32 (min(length, budget))."""
-    _on_current_device(key_weights=key_weights, seq_lens=seq_lens, kept=kept, new_lens=new_lens, err=err)
+    _on_current_device("key_weights seq_lens kept new_lens err", key_weights, seq_lens, kept, new_lens, err)
     _check_err(err)
     _check_i32(seq_lens, "seq_lens")
     budget, sink, recent = int(budget), int(sink), int(recent)
@@ -411,8 +417,9 @@ def evict_select(key_weights: torch.Tensor, seq_lens: torch.Tensor, budget: int,
     return kept, new_lens
 
 
-def _compact(call: str, c, block_tables, seq_lens, kept, key_weights, err, stream, **pools) -> None:
-    _on_current_device(block_tables=block_tables, seq_lens=seq_lens, kept=kept, key_weights=key_weights, err=err, **pools)
+def _compact(call: str, c, block_tables, seq_lens, kept, key_weights, err, stream, names: str, *pools) -> None:
+    _on_current_device("block_tables seq_lens kept key_weights err " + names, block_tables, seq_lens, kept, key_weights,
+                       err, *pools)
     _check_err(err)
     for t, n in ((block_tables, "block_tables"), (seq_lens, "seq_lens"), (kept, "kept")):
         _check_i32(t, n)
@@ -438,7 +445,7 @@ def evict_compact(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: to
     own (:meth:`BlockAllocator.unshare`); afterwards the lengths are
     min(length, budget) (:meth:`BlockAllocator.truncate`)."""
     _compact("pkv_evict_compact", _cache(k_cache, v_cache), block_tables, seq_lens, kept, key_weights, err, stream,
-             k_cache=k_cache, v_cache=v_cache)
+             "k_cache v_cache", k_cache, v_cache)
 
 
 def evict_compact_int8(kq: torch.Tensor, vq: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor,
@@ -447,7 +454,7 @@ def evict_compact_int8(kq: torch.Tensor, vq: torch.Tensor, k_scale: torch.Tensor
                        stream=None) -> None:
     """:func:`evict_compact` over an int8 cache: blocks in which rows of a head move are re-quantised."""
     _compact("pkv_evict_compact_int8", _cache_i8(kq, vq, k_scale, v_scale, torch.float16), block_tables, seq_lens, kept,
-             key_weights, err, stream, kq=kq, vq=vq, k_scale=k_scale, v_scale=v_scale)
+             key_weights, err, stream, "kq vq k_scale v_scale", kq, vq, k_scale, v_scale)
 
 
 def copy_blocks(k_caches: Sequence[torch.Tensor], v_caches: Sequence[torch.Tensor], src_dst_pairs: torch.Tensor,
