@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(32 * WARPS) evict_select_kernel(const SelectPa
             }
             __syncthreads();
             if (warp < TRIALS) {  // warp v: try v of this CTA, to every CTA of the row
-                const uint32_t c = sum(s_try[buf][lane][warp]);
+                const uint32_t c = sum(lane < WARPS ? s_try[buf][lane][warp] : 0u);
                 if (lane < p.cluster) *cg::this_cluster().map_shared_rank(&s_tries[buf][rank][warp], lane) = c;
             }
             cg::this_cluster().sync();
@@ -728,8 +728,9 @@ pkv_status pkv_evict_select(const float *weights, int64_t weights_seq_stride, in
     // the rows' capacity (the lengths are on the device) picks the size: up to
     // 4,096 keys to a CTA of four warps (2,048 rows of 512-4,096 keys, a CTA of
     // 1, 2, 4, 8 warps per row: 35, 29, 27, 31 us), 16,384 to one of eight,
-    // 131,072 to a cluster of eight CTAs of 32; beyond that the keys do not stay
-    // on chip
+    // 131,072 to a cluster of eight CTAs of 16 (16 rows of that length 32 us; 47
+    // with 32 warps, as not every cluster of eight 1,024-thread CTAs finds its
+    // SMs at once); beyond that the keys do not stay on chip
     constexpr int kSmem = 64 * 1024;
     static std::atomic<uint64_t> smem_set[3];
     if (max_keys <= 4096) {
@@ -747,14 +748,14 @@ pkv_status pkv_evict_select(const float *weights, int64_t weights_seq_stride, in
     } else {
         const int64_t parts = (max_keys + 16383) / 16384;
         p.cluster = parts <= 2 ? 2 : parts <= 4 ? 4 : kSelMaxCluster;
-        p.run_chunks = 4;
+        p.run_chunks = 8;
         const unsigned grid = (unsigned)(rows * p.cluster);
         if (parts <= kSelMaxCluster) {
-            st = set_smem_once(reinterpret_cast<const void *>(evict_select_kernel<32, true, true>), kSmem, &smem_set[2]);
+            st = set_smem_once(reinterpret_cast<const void *>(evict_select_kernel<16, true, true>), kSmem, &smem_set[2]);
             if (st != PKV_OK) return st;
-            st = launch_cluster(evict_select_kernel<32, true, true>, grid, 1024, p.cluster, kSmem, stream, p);
+            st = launch_cluster(evict_select_kernel<16, true, true>, grid, 512, p.cluster, kSmem, stream, p);
         } else {
-            st = launch_cluster(evict_select_kernel<32, true, false>, grid, 1024, p.cluster, 0, stream, p);
+            st = launch_cluster(evict_select_kernel<16, true, false>, grid, 512, p.cluster, 0, stream, p);
         }
     }
     return st == PKV_OK ? ok() : st;
