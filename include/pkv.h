@@ -340,9 +340,10 @@ PKV_API pkv_status pkv_attn_decode_int8(const void *q, int64_t q_token_stride, c
  * of pkv_attn_varlen_window, cache and arithmetic those of
  * pkv_attn_decode_int8 (rows of q_len == 1 are that call's).  In a chunk the
  * codes enter both matrix products exactly; k_scale multiplies the scores in
- * binary32, and v_scale the softmax weights, which enter P V as a bf16 hi + lo
- * pair (~16 significant bits) whatever the cache's dtype.  q and its row
- * stride must be 16-byte aligned when max_q_len > 1, 8-byte otherwise.
+ * binary32, and the softmax weights times v_scale enter P V as fp16 (11
+ * significant bits) in units of their row's largest, whatever the cache's dtype
+ * (a V scale under 2^-100 counts as 0).  q and its row stride must be 16-byte
+ * aligned when max_q_len > 1, 8-byte otherwise.
  */
 PKV_API pkv_status pkv_attn_varlen_int8(const void *q, int64_t q_token_stride, const pkv_cache_i8 *cache,
                                         const int32_t *block_tables, int32_t max_blocks_per_seq,
@@ -358,8 +359,9 @@ PKV_API pkv_status pkv_attn_varlen_int8(const void *q, int64_t q_token_stride, c
  * call, for every sequence s, KV head h and attended key t,
  *     weights[s][h][t] += sum over the query heads of h of softmax weight(t).
  * Keys outside the window, and entries at or past seq_lens[s], stay as they
- * were.  out is that of pkv_attn_decode_window / pkv_attn_decode_int8; other
- * arguments and errors are theirs.
+ * were.  out is that of pkv_attn_decode_window / pkv_attn_decode_int8 (int8 with
+ * fp16 queries: its last bits may differ, as the scores are not taken with that
+ * call's offset); other arguments and errors are theirs.
  *
  *   weights  device float32 [num_seqs, num_kv_heads, max_keys], entry (s, h, t)
  *            at s * weights_seq_stride + h * weights_head_stride + t, with
@@ -412,7 +414,7 @@ PKV_API pkv_status pkv_evict_select(const float *weights, int64_t weights_seq_st
  * L = seq_lens[s] > budget, row i < budget of KV head h becomes row
  * kept[s][h][i], in K, V and, where weights is not NULL, the weights, whose
  * entries budget .. L - 1 become 0.  seq_lens holds the lengths before the cut.
- * K and V rows at and past the budget are left as they were.  Heads keep
+ * K and V rows (int8: codes) at and past the budget are left as they were.  Heads keep
  * different tokens under one table, so a row of the pool no longer belongs to
  * one token; attention over the kept keys is unchanged (keys keep whatever
  * position their rotation gave them).
@@ -428,8 +430,8 @@ PKV_API pkv_status pkv_evict_select(const float *weights, int64_t weights_seq_st
  * int8: a block in which some row of the head moves is re-quantised from its
  * kept rows as pkv_write_kv_int8 does (value = code * scale, new scale =
  * max|value| * (1 / 127), code' = value / new scale rounded half to even, each
- * operation rounded to binary32); other blocks keep their codes and scales.  Supported: head_dim 64 or 128 (int8: 128),
- * block_size a multiple of 16 up to 256.
+ * operation rounded to binary32); other blocks keep their codes and scales.
+ * Supported: head_dim 64 or 128 (int8: 128), block_size a multiple of 16 up to 256.
  */
 PKV_API pkv_status pkv_evict_compact(const pkv_cache *cache, const int32_t *block_tables, int32_t max_blocks_per_seq,
                                      const int32_t *seq_lens, int32_t num_seqs, const int32_t *kept, int32_t budget,

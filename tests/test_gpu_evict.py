@@ -445,6 +445,64 @@ def test_refusals():
             P.evict_compact(**a)
 
 
+def test_offsets_past_32_bits():
+    """Pools of more than 2^32 bytes and weights whose rows lie 2^31 entries apart: decode with weights, selection, moves."""
+    hq, hkv, d, bs = 8, 8, 128, 16
+    nb = (1 << 32) // (bs * hkv * d * 2) + 64                   # 4.3 GB each
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    kc, vc = (torch.empty(nb, bs, hkv, d, dtype=torch.float16, device="cuda") for _ in range(2))
+    L, budget = 150, 40
+    ids = torch.tensor([[nb - 1 - 3 * i for i in range(10)], [nb - 2 - 3 * i for i in range(10)]], dtype=torch.int32, device="cuda")
+    for x in (kc, vc):
+        x[ids.long()] = torch.randn(2, 10, bs, hkv, d, generator=gen, device="cuda").half()
+    far = torch.zeros((1 << 31) + hkv * 160, device="cuda")
+    w = far.as_strided((2, hkv, 160), (1 << 31, 160, 1))
+    near = torch.zeros(2, hkv, 160, device="cuda")
+    lens = torch.tensor([L, L - 7], dtype=torch.int32, device="cuda")
+    q = torch.randn(2, hq, d, generator=gen, device="cuda").half()
+    # the same sequences in a small pool
+    small = torch.arange(20, dtype=torch.int32, device="cuda").view(2, 10)
+    ks, vs = kc[ids.long()].reshape(20, bs, hkv, d).clone(), vc[ids.long()].reshape(20, bs, hkv, d).clone()
+    a = P.attn_decode(q, kc, vc, ids, lens, d ** -0.5, key_weights=w)
+    b = P.attn_decode(q, ks, vs, small, lens, d ** -0.5, key_weights=near)
+    assert torch.equal(a, b) and torch.equal(w, near)
+    kept, _ = P.evict_select(w, lens, budget)
+    assert torch.equal(kept, P.evict_select(near, lens, budget)[0])
+    P.evict_compact(kc, vc, ids, lens, kept, key_weights=w)
+    P.evict_compact(ks, vs, small, lens, kept, key_weights=near)
+    assert torch.equal(w, near)
+    assert torch.equal(kc[ids.long()].reshape(20, bs, hkv, d), ks) and torch.equal(vc[ids.long()].reshape(20, bs, hkv, d), vs)
+
+
+def test_two_calls_at_once():
+    """Decode with weights, selection and moves of two batches on two streams, each with its own workspace."""
+    cases = [decode_case(60 + i, [900, 300, 31], 16, 8, 128, 16, "f16", poison=False).to("cuda") for i in range(2)]
+    keys = [c.tables.shape[1] * 16 for c in cases]
+
+    def run(c, n):
+        w = torch.zeros(3, 8, n, device="cuda")
+        ws = torch.empty(P.decode_workspace_size(3, 16, 8, 128, max_keys=n), dtype=torch.uint8, device="cuda")
+        k, v = c.k_cache.clone(), c.v_cache.clone()
+        for _ in range(5):
+            out = P.attn_decode(c.q, k, v, c.tables, c.lens, c.scale, key_weights=w, workspace=ws)
+        kept, new = P.evict_select(w, c.lens, 64, sink=2, recent=16)
+        P.evict_compact(k, v, c.tables, c.lens, kept, key_weights=w)
+        return out, w, kept, new, k, v
+
+    alone = [run(c, n) for c, n in zip(cases, keys)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    both = []
+    for c, n, st in zip(cases, keys, streams):
+        st.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(st):
+            both.append(run(c, n))
+    torch.cuda.synchronize()
+    for x, y in zip(alone, both):
+        for a, b in zip(x, y):
+            assert torch.equal(a, b)
+
+
 # ---- together --------------------------------------------------------------------
 
 def test_a_bounded_cache_over_many_steps():

@@ -192,6 +192,17 @@ def test_nothing_to_do():
     assert out.shape == (0, 16, 128)
 
 
+def test_rows_behind_the_last_sequence_stay():
+    """A padded step: query rows, outputs and tables past the sequences' own are neither read into results nor written."""
+    q, kq, vq, ks, vs, tab, cu, lens = _case(43, [40, 1, 33], [40, 90, 200], 16, 4, 16, "f16")
+    pad = torch.full((50, 16, 128), float("nan"), dtype=q.dtype)
+    out = torch.full((124, 16, 128), 7.0, device="cuda")
+    dev = [torch.from_numpy(x).cuda() for x in (kq, vq, ks, vs, tab, cu, lens)]
+    P.attn_varlen_int8(torch.cat([q, pad]).cuda(), *dev, 40, 128 ** -0.5, out=out)
+    _check((q, kq, vq, ks, vs, tab, cu, lens), 128 ** -0.5, got=out[:74])
+    assert (out[74:] == 7.0).all()
+
+
 def test_same_bits_every_time_and_replayed():
     case = _case(31, [257, 1, 66], [700, 90, 66], 32, 8, 32, "bf16")
     q, *rest = case
