@@ -1089,9 +1089,10 @@ constexpr int kWeightKeys = kWeightThreads * kWeightsPerThread;
 template <int G>
 __device__ __forceinline__ void add_key_weights(const DecodeParams &p, int64_t row, int chunk) {
     __shared__ float2 s_norm[G];
+    __shared__ int s_cut[3];  // first and last part of the sequence, record slot of the first
     const int64_t s = row / p.hkv;
     const int h = (int)(row - s * p.hkv);
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     pdl_wait();
     pdl_trigger();
     // two rounds of loads: the lengths and the split, then scores, weights and records
@@ -1101,25 +1102,27 @@ __device__ __forceinline__ void add_key_weights(const DecodeParams &p, int64_t r
     const int first = decode_first_key(p, L);
     const int t0 = chunk * kWeightKeys;
     if (L > cap || t0 >= L || t0 + kWeightKeys <= first) return;
-    const float *sp = p.scores + row * cap * G;
-    float *w = p.key_w + s * p.w_seq + h * p.w_head;
+    const int mine = t0 + tid;
+    const float *xp = p.scores + (row * cap + mine) * G;
+    float *wp = p.key_w + s * p.w_seq + h * p.w_head + mine;
+    // the thread's keys mine + 256 u that are attended
+    auto seen = [&](int u) { return mine + u * kWeightThreads < L && mine + u * kWeightThreads >= first; };
     float x[kWeightsPerThread][G], old[kWeightsPerThread];
 #pragma unroll
     for (int u = 0; u < kWeightsPerThread; ++u) {
-        const int t = t0 + u * kWeightThreads + tid;
-        if (t >= L || t < first) continue;
-        old[u] = w[t];
-        const float *xp = sp + (int64_t)t * G;
+        if (!seen(u)) continue;
+        old[u] = wp[u * kWeightThreads];
+        const float *xu = xp + u * kWeightThreads * G;
         if constexpr (G == 1) {
-            x[u][0] = xp[0];
+            x[u][0] = xu[0];
         } else if constexpr (G == 2) {
-            const float2 a = *reinterpret_cast<const float2 *>(xp);
+            const float2 a = *reinterpret_cast<const float2 *>(xu);
             x[u][0] = a.x;
             x[u][1] = a.y;
         } else {
 #pragma unroll
             for (int i = 0; i < G; i += 4) {
-                const float4 a = *reinterpret_cast<const float4 *>(xp + i);
+                const float4 a = *reinterpret_cast<const float4 *>(xu + i);
                 x[u][i] = a.x;
                 x[u][i + 1] = a.y;
                 x[u][i + 2] = a.z;
@@ -1127,15 +1130,27 @@ __device__ __forceinline__ void add_key_weights(const DecodeParams &p, int64_t r
             }
         }
     }
-    // the row's norms, joined from the records where the sequence was cut
-    const bool whole = whole_seq_split(total, p.num_seqs, p.grid_x, p.whole_max);
-    const int c0 = whole ? 0 : range_owner(start, total, ctas), c1 = whole ? 0 : range_owner(start + n - 1, total, ctas);
-    const int warp = tid >> 5, lane = tid & 31;
+    // the row's norms, joined from the records where the sequence was cut (the
+    // split's 64-bit divisions by one warp: by all they were a third of the kernel)
+    if (warp == 0) {
+        int c0 = 0, c1 = 0, slot0 = 0;
+        if (!whole_seq_split(total, p.num_seqs, p.grid_x, p.whole_max)) {
+            c0 = range_owner(start, total, ctas);
+            c1 = range_owner(start + n - 1, total, ctas);
+            slot0 = start == (int64_t)c0 * total / ctas ? 0 : 1;
+        }
+        if (lane == 0) {
+            s_cut[0] = c0;
+            s_cut[1] = c1;
+            s_cut[2] = slot0;
+        }
+    }
+    __syncthreads();
     if (warp < G) {
+        const int c0 = s_cut[0], c1 = s_cut[1], slot0 = s_cut[2];
         if (c0 == c1) {
             if (lane == 0) s_norm[warp] = p.norm[row * G + warp];
         } else {
-            const int slot0 = start == (int64_t)c0 * total / ctas ? 0 : 1;
             const int hgi = h / p.heads_per_cta, hl = (h - hgi * p.heads_per_cta) * G + warp;
             float M = -INFINITY, l = 0.f;
             for (int c = c0 + lane; c <= c1; c += 32) {
@@ -1161,24 +1176,25 @@ __device__ __forceinline__ void add_key_weights(const DecodeParams &p, int64_t r
     for (int i = 0; i < G; ++i) nm[i] = s_norm[i];
 #pragma unroll
     for (int u = 0; u < kWeightsPerThread; ++u) {
-        const int t = t0 + u * kWeightThreads + tid;
-        if (t >= L || t < first) continue;
+        if (!seen(u)) continue;
         float sum = 0.f;
 #pragma unroll
-        for (int i = 0; i < G; ++i) sum += fast_exp2(x[u][i] - nm[i].x) * nm[i].y;
-        w[t] = old[u] + sum;
+        for (int i = 0; i < G; ++i) sum = fmaf(fast_exp2(x[u][i] - nm[i].x), nm[i].y, sum);
+        wp[u * kWeightThreads] = old[u] + sum;
     }
 }
 
-// The merge and the key weights of a call in one launch: the first `merges`
-// CTAs merge (sequence fastest), the others take key_chunks chunks per row.
+// The merge and the key weights of a call in one launch: `merges` CTAs merge
+// (sequence fastest), spread evenly among those that take key_chunks chunks per
+// row, so that the merges' latency passes under the others' traffic.
 template <int D, typename T, int kMergeHeads, int G>
 __global__ void __launch_bounds__(kMergeThreads) decode_finish_kernel(const DecodeParams p, const int merges,
                                                                       const int key_chunks) {
-    if ((int)blockIdx.x < merges) {
-        merge_parts<D, T, kMergeHeads>(p, blockIdx.x % p.num_seqs, blockIdx.x / p.num_seqs);
+    const int m = (int)((int64_t)blockIdx.x * merges / gridDim.x);  // merges before this CTA
+    if ((int)((int64_t)(blockIdx.x + 1) * merges / gridDim.x) > m) {
+        merge_parts<D, T, kMergeHeads>(p, m % p.num_seqs, m / p.num_seqs);
     } else {
-        const int i = blockIdx.x - merges;
+        const int i = blockIdx.x - m;
         add_key_weights<G>(p, i / key_chunks, i % key_chunks);
     }
 }
