@@ -126,6 +126,8 @@ struct DecodeParams {
     int64_t w_seq, w_head;
     float *scores;                 // workspace [num_seqs][hkv][max_blocks * block_size][group], in base 2
     float2 *norm;                  // workspace [num_seqs][hq]: (max, 1 / sum) of rows finished by the decode kernel
+    int2 *cut;                     // workspace [num_seqs]: 2 * first CTA + its record slot and the last CTA of a cut
+                                   // sequence, or (-1, -1)
 };
 
 // First key a decode row of a sequence with L keys attends (sliding window).
@@ -819,6 +821,7 @@ __global__ void __launch_bounds__(cta_threads<D, I8>(), I8 ? kI8CtasPerSm : (D =
         if (complete) {
             const float iA = 1.f / lA, iB = 1.f / lB;
             if constexpr (W) {
+                if (hg == 0 && w == 0 && lane == 0) p.cut[s] = make_int2(-1, -1);
                 if (g == 0) {
                     float2 *nm = p.norm + (int64_t)s * p.hkv * G + kvh * G;
                     if (hA < G) nm[hA] = make_float2(mA, iA);
@@ -853,6 +856,12 @@ __global__ void __launch_bounds__(cta_threads<D, I8>(), I8 ? kI8CtasPerSm : (D =
             }
         } else {
             const int slot = first_seg ? 0 : 1;
+            if constexpr (W) {  // every head group is cut alike
+                if (hg == 0 && w == 0 && lane == 0) {
+                    if (sb == 0) p.cut[s].x = 2 * blockIdx.x + slot;
+                    if (b1 == n_s) p.cut[s].y = blockIdx.x;
+                }
+            }
             const int64_t rec = (((int64_t)hg * p.cmax + blockIdx.x) * 2 + slot) * qheads_cta + (int64_t)w * G;
             float *wo = p.ws_o + rec * D;
             float *wml = p.ws_ml + rec * 2;
@@ -1089,15 +1098,14 @@ constexpr int kWeightKeys = kWeightThreads * kWeightsPerThread;
 template <int G>
 __device__ __forceinline__ void add_key_weights(const DecodeParams &p, int64_t row, int chunk) {
     __shared__ float2 s_norm[G];
-    __shared__ int s_cut[3];  // first and last part of the sequence, record slot of the first
     const int64_t s = row / p.hkv;
     const int h = (int)(row - s * p.hkv);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     pdl_wait();
     pdl_trigger();
-    // two rounds of loads: the lengths and the split, then scores, weights and records
+    // two rounds of loads: the length and the cut, then scores, weights and records
     const int L = p.seq_lens[s];
-    const int64_t total = p.ws_meta[0], ctas = p.ws_meta[1], start = p.ws_meta[2 + s], n = p.ws_meta[3 + s] - start;
+    const int2 cut = p.cut[s];
     const int64_t cap = (int64_t)p.max_blocks * p.block_size;
     const int first = decode_first_key(p, L);
     const int t0 = chunk * kWeightKeys;
@@ -1130,43 +1138,28 @@ __device__ __forceinline__ void add_key_weights(const DecodeParams &p, int64_t r
             }
         }
     }
-    // the row's norms, joined from the records where the sequence was cut (the
-    // split's 64-bit divisions by one warp: by all they were a third of the kernel)
-    if (warp == 0) {
-        int c0 = 0, c1 = 0, slot0 = 0;
-        if (!whole_seq_split(total, p.num_seqs, p.grid_x, p.whole_max)) {
-            c0 = range_owner(start, total, ctas);
-            c1 = range_owner(start + n - 1, total, ctas);
-            slot0 = start == (int64_t)c0 * total / ctas ? 0 : 1;
-        }
-        if (lane == 0) {
-            s_cut[0] = c0;
-            s_cut[1] = c1;
-            s_cut[2] = slot0;
-        }
-    }
-    __syncthreads();
+    // the row's norms, joined from the records where the sequence was cut
     if (warp < G) {
-        const int c0 = s_cut[0], c1 = s_cut[1], slot0 = s_cut[2];
-        if (c0 == c1) {
+        if (cut.x < 0) {
             if (lane == 0) s_norm[warp] = p.norm[row * G + warp];
         } else {
-            const int hgi = h / p.heads_per_cta, hl = (h - hgi * p.heads_per_cta) * G + warp;
-            float M = -INFINITY, l = 0.f;
-            for (int c = c0 + lane; c <= c1; c += 32) {
-                const int64_t rec = (((int64_t)hgi * p.cmax + c) * 2 + (c == c0 ? slot0 : 0)) * (p.heads_per_cta * G) + hl;
-                const float2 ml = *reinterpret_cast<const float2 *>(p.ws_ml + rec * 2);
-                const float m = fmaxf(M, ml.x);
-                l = l * exp2f(M - m) + ml.y * exp2f(ml.x - m);
-                M = m;
+            const int c0 = cut.x >> 1, hgi = h / p.heads_per_cta, hl = (h - hgi * p.heads_per_cta) * G + warp;
+            auto record = [&](int c) {
+                const int64_t r = (((int64_t)hgi * p.cmax + c) * 2 + (c == c0 ? cut.x & 1 : 0)) * (p.heads_per_cta * G) + hl;
+                return *reinterpret_cast<const float2 *>(p.ws_ml + r * 2);
+            };
+            const float2 mine1 = c0 + lane <= cut.y ? record(c0 + lane) : make_float2(-INFINITY, 0.f);
+            float M = mine1.x;
+            for (int c = c0 + 32 + lane; c <= cut.y; c += 32) M = fmaxf(M, record(c).x);
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+            float l = mine1.y * exp2f(mine1.x - M);
+            for (int c = c0 + 32 + lane; c <= cut.y; c += 32) {
+                const float2 ml = record(c);
+                l += ml.y * exp2f(ml.x - M);
             }
 #pragma unroll
-            for (int off = 16; off > 0; off >>= 1) {
-                const float m2 = __shfl_xor_sync(0xffffffffu, M, off), l2 = __shfl_xor_sync(0xffffffffu, l, off);
-                const float m = fmaxf(M, m2);
-                l = (M == -INFINITY ? 0.f : l * exp2f(M - m)) + (m2 == -INFINITY ? 0.f : l2 * exp2f(m2 - m));
-                M = m;
-            }
+            for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
             if (lane == 0) s_norm[warp] = make_float2(M, 1.f / l);
         }
     }
@@ -1319,16 +1312,19 @@ static pkv_status launch_decode_t(const CUtensorMap &mk, const CUtensorMap &mv, 
     return PKV_OK;
 }
 
-// Workspace of the key weights behind the decode plan's: norms, then scores.
+// Workspace of the key weights behind the decode plan's: cuts, norms, then scores.
 static size_t weights_bytes(int32_t num_seqs, int32_t num_q_heads, int64_t max_keys) {
     const size_t rows = (size_t)num_seqs * num_q_heads;
-    return round256(rows * sizeof(float2)) + round256(rows * (size_t)max_keys * sizeof(float));
+    return round256((size_t)num_seqs * sizeof(int2)) + round256(rows * sizeof(float2)) +
+           round256(rows * (size_t)max_keys * sizeof(float));
 }
 
 static void set_key_weights(DecodeParams *p, const KeyWeights &kw, uint8_t *ws, int32_t num_q_heads) {
     p->key_w = kw.w;
     p->w_seq = kw.seq_stride;
     p->w_head = kw.head_stride;
+    p->cut = reinterpret_cast<int2 *>(ws);
+    ws += round256((size_t)p->num_seqs * sizeof(int2));
     p->norm = reinterpret_cast<float2 *>(ws);
     p->scores = reinterpret_cast<float *>(ws + round256((size_t)p->num_seqs * num_q_heads * sizeof(float2)));
 }
