@@ -365,7 +365,8 @@ PKV_API pkv_status pkv_attn_varlen_int8(const void *q, int64_t q_token_stride, c
  *
  *   weights  device float32 [num_seqs, num_kv_heads, max_keys], entry (s, h, t)
  *            at s * weights_seq_stride + h * weights_head_stride + t, with
- *            max_keys = max_blocks_per_seq * block_size; rows do not overlap.
+ *            max_keys = max_blocks_per_seq * block_size, at most 2^30; rows do not
+ *            overlap.
  *   workspace >= pkv_attn_decode_weights_workspace_size bytes: the decode
  *            workspace and 4 bytes per (query head, key of the tables' capacity).
  *
@@ -402,7 +403,8 @@ PKV_API pkv_status pkv_attn_decode_int8_weights(const void *q, int64_t q_token_s
  *             then -1.
  *   new_lens  device int32 [num_seqs]: min(L, budget); not the seq_lens array.
  * A length below 0 or above max_keys sets PKV_DEVERR_LENGTH: kept is all -1 and
- * new_lens the length as it is.  budget > 0, sink + recent <= budget.
+ * new_lens the length as it is.  0 < budget <= 2^30, sink + recent <= budget,
+ * max_keys <= 2^30.
  */
 PKV_API pkv_status pkv_evict_select(const float *weights, int64_t weights_seq_stride, int64_t weights_head_stride,
                                     int64_t max_keys, const int32_t *seq_lens, int32_t num_seqs,
@@ -431,7 +433,8 @@ PKV_API pkv_status pkv_evict_select(const float *weights, int64_t weights_seq_st
  * kept rows as pkv_write_kv_int8 does (value = code * scale, new scale =
  * max|value| * (1 / 127), code' = value / new scale rounded half to even, each
  * operation rounded to binary32); other blocks keep their codes and scales.
- * Supported: head_dim 64 or 128 (int8: 128), block_size a multiple of 16 up to 256.
+ * Supported: head_dim 64 or 128 (int8: 128), block_size a multiple of 16 up to
+ * 256, max_blocks_per_seq * block_size and budget at most 2^30.
  */
 PKV_API pkv_status pkv_evict_compact(const pkv_cache *cache, const int32_t *block_tables, int32_t max_blocks_per_seq,
                                      const int32_t *seq_lens, int32_t num_seqs, const int32_t *kept, int32_t budget,

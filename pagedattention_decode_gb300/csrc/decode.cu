@@ -1633,7 +1633,7 @@ pkv_status pkv_attn_decode_int8(const void *q, int64_t q_token_stride, const pkv
 pkv_status pkv_attn_decode_weights_workspace_size(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
                                                   int32_t head_dim, int64_t max_keys, int32_t device, size_t *bytes) {
     PKV_CHECK_ARG(bytes && num_seqs >= 0 && num_kv_heads > 0 && num_q_heads > 0 && head_dim > 0 && max_keys >= 0 &&
-                      max_keys < (int64_t)1 << 31,
+                      max_keys <= kMaxRowKeys,
                   PKV_ERR_INVALID_ARG, "bad argument");
     pkv_status st = decode_workspace_size_any(num_seqs, num_q_heads, num_kv_heads, head_dim, device, bytes);
     if (st != PKV_OK) return st;
@@ -1648,7 +1648,7 @@ static pkv_status check_key_weights(const float *weights, int64_t seq_stride, in
     PKV_CHECK_ARG((reinterpret_cast<uintptr_t>(weights) & 3) == 0, PKV_ERR_INVALID_ARG,
                   "%s: weights must be 4-byte aligned", what);
     const int64_t keys = (int64_t)max_blocks * bs;
-    PKV_CHECK_ARG(keys < (int64_t)1 << 31, PKV_ERR_SHAPE, "%s: tables cover 2^31 keys or more", what);
+    PKV_CHECK_ARG(keys <= kMaxRowKeys, PKV_ERR_SHAPE, "%s: tables cover more than 2^30 keys", what);
     PKV_CHECK_ARG(head_stride >= keys && seq_stride >= (hkv - 1) * head_stride + keys, PKV_ERR_SHAPE,
                   "%s: weights rows shorter than the tables' %lld keys, or overlapping", what, (long long)keys);
     PKV_CHECK_ARG((keys / kWeightKeys + 9) * num_seqs * hkv < (int64_t)1 << 31, PKV_ERR_UNSUPPORTED,

@@ -14,6 +14,9 @@ namespace pkv {
 
 inline int dtype_bytes(int32_t dt) { return dt == PKV_F32 ? 4 : (dt == PKV_F16 || dt == PKV_BF16) ? 2 : 0; }
 
+// Keys of one row of accumulated weights: positions plus a CTA's stride stay below 2^31.
+constexpr int64_t kMaxRowKeys = (int64_t)1 << 30;
+
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 #define PKV_CUDA_TRY(expr)                                                              \

@@ -42,6 +42,10 @@
 // All 512 TMEM columns (per tile: S/P 128, O head_dim) and ~217 KB of shared
 // memory; setmaxnreg moves registers from the producer / MMA warpgroup
 // (warps 0-3) to the two softmax warpgroups.
+//
+// Over an int8 cache (template argument I8) a fourth warpgroup (warps 12-15)
+// converts the codes that the producer stages into the swizzled tiles, the
+// softmax applies the scales, and registers are not moved.
 #include <cuda.h>
 
 #include <cstring>
@@ -482,8 +486,9 @@ __global__ void __launch_bounds__(Regs<I8>::kThreads, 1)
     __shared__ TcItem s_item[2];
     __shared__ uint32_t s_tmem;
     __shared__ volatile int s_abort;
-    // int8: the scales of the 16-token sub-blocks of a step, slot = step % 4.  The fill of step g + 4 follows the release of step
-    // g + 3's K, whose score MMAs follow the softmax of step g + 2.
+    // int8: the scales of the 16-token sub-blocks of a step, slot = step % 4.  The fill of step g + 4 follows the
+    // conversion of step g + 3's K, which waits for the score MMAs of step g + 2 to have read the stage; those follow
+    // the softmax of step g + 1.
     __shared__ __align__(16) StepScales s_scales[I8 ? 4 : 1];
     uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t *sq = base;
@@ -761,7 +766,10 @@ __global__ void __launch_bounds__(Regs<I8>::kThreads, 1)
                     // a V scale too small for 1 / scale (0 among them: values under 2^-93) counts as 0:
                     // its codes are multiplied by 0, its P by a scale of 1
                     const bool zero = fabsf(vs) < 7.8886091e-31f;  // 2^-100
-                    const float lv = zero ? 0.f : log2f(fabsf(vs)), iv = zero ? 1.f : 1.f / fabsf(vs);
+                    // a scale that is not finite reaches the rows that see its keys through lv alone: masked
+                    // keys enter a row's sum as 0 * iv
+                    const float lv = zero ? 0.f : log2f(fabsf(vs));
+                    const float iv = !zero && fabsf(vs) < INFINITY ? 1.f / fabsf(vs) : 1.f;
                     lookup(j + 1);
                     const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, mine)) * box * 128;
 #pragma unroll

@@ -8,7 +8,8 @@
 //
 // Rows of sequences with q_len == 1 are decode rows and run through the
 // split-K decode kernel (decode.cu); chunks with q_len > 1 run on the tcgen05
-// tile kernel (prefill_tc.cu).  This file holds the C ABI entry points.
+// tile kernel (prefill_tc.cu), both for 16-bit and int8 caches.  This file holds
+// the C ABI entry points.
 #include <cuda.h>
 
 #include "launch.h"

@@ -184,3 +184,42 @@ def _weights(i8=False, **k):
     (dict(n=0, w=None), 0)])
 def test_weights_refusals(i8, change, status):
     assert _weights(i8, **change) == status, _native.lib().pkv_last_error()
+
+
+MANY = (1 << 30) + 16  # positions are 32-bit: a row of more than 2^30 keys, or a budget above that, is refused
+
+
+def test_rows_past_2_30_keys_are_refused():
+    assert _select(keys=MANY, sh=MANY, ss=2 * MANY) == 3
+    assert _select(budget=MANY) == 3 and _select(budget=2 ** 31 - 1) == 3
+    for i8 in (False, True):
+        c = _c8() if i8 else _c16()
+        assert _compact(c, i8, mb=MANY // 16, w=None) == 3
+        assert _compact(c, i8, budget=MANY) == 3 and _compact(c, i8, budget=2 ** 31 - 1) == 3
+        assert _weights(i8, mb=MANY // 16, sh=1 << 33, ss=1 << 36) == 3
+    n = ctypes.c_size_t()
+    assert _native.lib().pkv_attn_decode_weights_workspace_size(1, 8, 4, 128, MANY, 0, ctypes.byref(n)) != 0
+
+
+def _varlen8(cache=None, **k):
+    a = dict(q=FAKE, stride=8 * 128, tables=FAKE, mb=4, cu=FAKE, lens=FAKE, n=3, total=9, longest=4, hq=8, out=FAKE, dtype=2,
+             ws=FAKE, ws_bytes=0)
+    a.update(k)
+    return _native.lib().pkv_attn_varlen_int8(a["q"], a["stride"], ctypes.byref(cache or _c8()), a["tables"], a["mb"], a["cu"],
+                                              a["lens"], a["n"], a["total"], a["longest"], a["hq"], 1.0, 1, 0, a["out"],
+                                              a["dtype"], a["ws"], a["ws_bytes"], None, None)
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(n=-1), 1), (dict(total=-1), 1), (dict(longest=-1), 1), (dict(mb=-1), 1), (dict(q=None), 1), (dict(tables=None), 1),
+    (dict(cu=None), 1), (dict(lens=None), 1), (dict(out=None), 1), (dict(out=FAKE + 8), 1), (dict(q=FAKE + 4), 1),
+    (dict(stride=8 * 128 - 2), 1), (dict(hq=6), 3), (dict(hq=12), 9), (dict(dtype=1), 2), (dict(n=65536), 9),
+    (dict(n=0), 0), (dict(total=0, q=None, cu=None), 0)])
+def test_varlen_int8_refusals(change, status):
+    assert _varlen8(**change) == status, _native.lib().pkv_last_error()
+
+
+def test_varlen_int8_refuses_caches_it_was_not_built_for():
+    assert _varlen8(_c8(d=64), stride=8 * 64) == 9
+    assert _varlen8(_c8(hkv=2)) == 9
+    assert _varlen8(_c8(bs=24)) == 9

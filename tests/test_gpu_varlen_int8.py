@@ -150,6 +150,26 @@ def test_zero_blocks_and_values_that_are_not_seen():
     assert int(err) == 0 and (np.abs(out.cpu().double().numpy() - want) <= bound).all()
 
 
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+@pytest.mark.parametrize("which", ["k", "v", "both"])
+def test_scales_that_are_not_finite_stay_with_the_rows_that_see_them(which, bad):
+    """A block of the chunk itself with such a scale: the rows before it are as if it were not there."""
+    case = _case(29, [300], [420], 16, 4, 16, "f16")
+    q, kq, vq, ks, vs, tab, cu, lens = case
+    want, bound = _reference(*case, 128 ** -0.5)
+    first = 20 * 16 - 120                      # the first row that sees a key of block 20
+    blk = tab[0, 20]
+    if which != "v":
+        ks[blk] = bad
+    if which != "k":
+        vs[blk] = bad
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = _run(case, 128 ** -0.5, err=err).cpu().double().numpy()
+    assert int(err) == 0 and (np.abs(out - want) <= bound)[:first].all()
+    if which != "k" or math.isnan(bad):        # (an infinite K scale: scores of -inf leave a row finite)
+        assert not np.isfinite(out[first:]).all(axis=-1).any()
+
+
 def test_scales_of_any_sign_and_zero_over_codes():
     """Scales are plain factors: negative ones, zeros over codes that are not zero, and V scales from 1e-3 to 10 in one row."""
     case = _case(41, [150, 3], [600, 333], 16, 4, 16, "f16")
