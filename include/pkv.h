@@ -341,7 +341,7 @@ PKV_API pkv_status pkv_attn_decode_int8(const void *q, int64_t q_token_stride, c
  * pkv_attn_decode_int8 (rows of q_len == 1 are that call's).  In a chunk the
  * codes enter both matrix products exactly; k_scale multiplies the scores in
  * binary32, and the softmax weights times v_scale enter P V as fp16 (11
- * significant bits) in units of their row's largest, whatever the cache's dtype
+ * significant bits) in units of at most their row's largest, whatever the cache's dtype
  * (a V scale under 2^-100 counts as 0).  q and its row stride must be 16-byte
  * aligned when max_q_len > 1, 8-byte otherwise.
  */

@@ -322,8 +322,8 @@ constexpr int kCodeBytes = 2 * kTok * 128;
 // and MMA warps spill 96 bytes and the softmax 28 more.  88 / 208 took the
 // mixed step's prefill chunks from 1,075 to 1,121 TFLOP/s (A/B on one box).
 //
-// int8 caches add a warpgroup that converts codes: 512 threads of 128
-// registers, enough for every role there, nothing re-balanced.
+// int8 caches add a warpgroup that converts codes: 512 threads, at most 128
+// registers each, enough for every role there, nothing re-balanced.
 template <bool I8>
 struct Regs {
     static constexpr int kThreads = I8 ? 512 : 384;
@@ -353,32 +353,45 @@ struct StepScales {
 // with M a running maximum of score + log2 vscale; the row's sum takes each
 // sub-block's P back by 1 / vscale.
 // Unlike the 16-bit step below, which holds a row's scores in registers, this
-// one reads 32 at a time and holds P (64 registers), so that with a fourth
-// warpgroup every thread fits the 128 registers of a 512-thread launch (a row
-// of scores spilled 664 bytes).  The scores stay in TMEM until the step's P sum
-// to at most 2^15, which proves every P finite as fp16: M comes from the row's
-// first visible keys and is taken again, O and the sum scaled down and P
-// computed once more, only where they do not.
+// one takes 32 keys at a time in a loop that is not unrolled: the converting
+// warps' code competes for the instruction cache, and 95 registers a thread
+// leave room for a fourth warpgroup (16 chunks of 512 rows over 2,560 keys: 320
+// us; two parts unrolled 323, four 361; P of the whole step in registers 327,
+// there with the loads a part ahead and 176 registers 335; two warps per 32 rows
+// 345; eight converting warps 330).
+// P of keys 32 c .. 32 c + 31 goes to columns 16 c .. 16 c + 15, whose scores
+// were read.  M comes from the row's first visible keys and is taken again only
+// where a part's P sum to more than 2^15 (their sum proves every P finite as
+// fp16): then O, the sum and the P already stored are scaled down, by a power of
+// two, which is exact down to fp16's smallest step, and the part is computed
+// once more.
 // hi_c, lo_c: the row sees the step's keys lo_c .. hi_c.
 template <int D>
 __device__ __forceinline__ void softmax_step_i8(uint32_t trow, const StepScales &scl, bool whole, int hi_c, int lo_c,
                                                 bool has_o, float &m_used, float &lsum) {
-    // M becomes the largest of the step's visible keys on the lanes that ask
-    auto raise = [&](bool ask) {
+    constexpr int kPart = 32;
+    // M of the lanes that ask moves to the largest of the visible keys from part cc on (the parts before it are P
+    // already), or, where there is something to scale, by the whole powers of two towards it (2^10 or more: 32
+    // keys sum to more than 2^15)
+    auto raise = [&](bool ask, int cc) {
+        tmem_wait_st();
         float most = -INFINITY;
 #pragma unroll 1
-        for (int cc = 0; cc < kTok / 8; ++cc) {
+        for (int c0 = kPart * cc; c0 < kTok; c0 += 8) {
             uint32_t sr[8];
-            tmem_ld8(trow + 8 * cc, sr);
+            tmem_ld8(trow + c0, sr);
             tmem_wait_ld();
 #pragma unroll
             for (int c = 0; c < 8; ++c)
-                if (8 * cc + c <= hi_c && 8 * cc + c >= lo_c)
-                    most = fmaxf(most, fmaf(__uint_as_float(sr[c]), scl.k[cc >> 1], scl.lv[cc >> 1]));
+                if (c0 + c <= hi_c && c0 + c >= lo_c)
+                    most = fmaxf(most, fmaf(__uint_as_float(sr[c]), scl.k[c0 >> 4], scl.lv[c0 >> 4]));
         }
-        const float m_new = ask ? fmaxf(m_used, most) : m_used;
-        const float alpha = m_new > m_used ? fast_exp2(m_used - m_new) : 1.f;
-        m_used = m_new;
+        float alpha = 1.f;
+        if (ask && most > m_used) {
+            const float up = floorf(most - m_used);
+            alpha = up < 126.f ? __int_as_float((127 - (int)up) << 23) : 0.f;
+            m_used = m_used == -INFINITY ? most : m_used + up;
+        }
         lsum *= alpha;
         if (has_o) {
 #pragma unroll 1
@@ -390,61 +403,85 @@ __device__ __forceinline__ void softmax_step_i8(uint32_t trow, const StepScales 
                 for (int i = 0; i < 8; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
                 tmem_st8(trow + 128 + c0, o);
             }
-            tmem_wait_st();
         }
-    };
-    const bool fresh = m_used == -INFINITY && hi_c >= 0 && lo_c < kTok;
-    if (__any_sync(0xffffffffu, fresh)) raise(fresh);
-    uint32_t ph[kTok / 2];
-    float step_sum;
 #pragma unroll 1
-    for (int pass = 0;; ++pass) {
-        // a row that has met no key yet: every score and m_used are -inf, P = 0
-        const float neg_m = m_used == -INFINITY ? -INFINITY : -m_used;
-        float total = 0.f;
-        step_sum = 0.f;
-#pragma unroll
-        for (int cc = 0; cc < kTok / 32; ++cc) {
-            uint32_t sr[32];
-            tmem_ld32(trow + 32 * cc, sr);
+        for (int c0 = 0; c0 < kPart / 2 * cc; c0 += 8) {
+            uint32_t o[8];
+            tmem_ld8(trow + c0, o);
             tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float2 v = unpack2<__half>(o[i]);
+                o[i] = pack2<__half>(v.x * alpha, v.y * alpha);
+            }
+            tmem_st8(trow + c0, o);
+        }
+        tmem_wait_st();
+    };
+    if (whole && !has_o) {
+        // the item's first step, all of it visible: M from its first 32 keys
+        uint32_t sr[32];
+        tmem_ld32(trow, sr);
+        tmem_wait_ld();
+        float x0 = -INFINITY, x1 = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+            x0 = fmaxf(x0, __uint_as_float(sr[c]) * scl.k[0]);
+            x1 = fmaxf(x1, __uint_as_float(sr[16 + c]) * scl.k[1]);
+        }
+        m_used = fmaxf(x0 + scl.lv[0], x1 + scl.lv[1]);
+    }
+    const bool fresh = m_used == -INFINITY && hi_c >= 0 && lo_c < kTok;
+    if (__any_sync(0xffffffffu, fresh)) raise(fresh, 0);
+#pragma unroll 1
+    for (int cc = 0; cc < kTok / kPart; ++cc) {
+        uint32_t ph[kPart / 2];
+        float part_sum;
+#pragma unroll 1
+        for (int pass = 0;; ++pass) {
+            uint32_t sr[kPart];
+            tmem_ld32(trow + kPart * cc, sr);
             const float2 ks = *reinterpret_cast<const float2 *>(&scl.k[2 * cc]);
             const float2 lv = *reinterpret_cast<const float2 *>(&scl.lv[2 * cc]);
             const float2 iv = *reinterpret_cast<const float2 *>(&scl.iv[2 * cc]);
+            // a row that has met no key yet: every score and m_used are -inf, P = 0
+            const float neg_m = m_used == -INFINITY ? -INFINITY : -m_used;
+            const float2 add = make_float2(lv.x + neg_m, lv.y + neg_m);
+            tmem_wait_ld();
 #pragma unroll
-            for (int c = 0; c < 32; c += 2) {
-                const float k = c < 16 ? ks.x : ks.y, add = (c < 16 ? lv.x : lv.y) + neg_m;
+            for (int c = 0; c < kPart; c += 2) {
+                const float k = c < 16 ? ks.x : ks.y, a = c < 16 ? add.x : add.y;
                 const float2 x = __ffma2_rn(make_float2(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])),
-                                            make_float2(k, k), make_float2(add, add));
+                                            make_float2(k, k), make_float2(a, a));
                 sr[c] = __float_as_uint(x.x);
                 sr[c + 1] = __float_as_uint(x.y);
             }
             if (!whole) {
+                const int hi = hi_c - kPart * cc, lo = lo_c - kPart * cc;
 #pragma unroll
-                for (int c = 0; c < 32; ++c)
-                    if (32 * cc + c > hi_c || 32 * cc + c < lo_c) sr[c] = __float_as_uint(-INFINITY);
+                for (int c = 0; c < kPart; ++c)
+                    if (c > hi || c < lo) sr[c] = __float_as_uint(-INFINITY);
             }
+            float2 sum[2];
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
-                float2 sum = make_float2(0.f, 0.f);
+                sum[b] = make_float2(0.f, 0.f);
 #pragma unroll
                 for (int c = 16 * b; c < 16 * b + 16; c += 2) {
                     const float2 pr = make_float2(fast_exp2(__uint_as_float(sr[c])), fast_exp2(__uint_as_float(sr[c + 1])));
-                    sum = __fadd2_rn(sum, pr);
-                    ph[16 * cc + c / 2] = pack2<__half>(pr.x, pr.y);
+                    sum[b] = __fadd2_rn(sum[b], pr);
+                    ph[c / 2] = pack2<__half>(pr.x, pr.y);
                 }
-                const float both = sum.x + sum.y;
-                total += both;
-                step_sum = fmaf(both, b ? iv.y : iv.x, step_sum);
             }
+            const float s0 = sum[0].x + sum[0].y, s1 = sum[1].x + sum[1].y;
+            part_sum = fmaf(s1, iv.y, s0 * iv.x);
+            const bool over = pass == 0 && !(s0 + s1 <= kPSumMax);
+            if (!__any_sync(0xffffffffu, over)) break;
+            raise(over, cc);
         }
-        const bool over = pass == 0 && !(total <= kPSumMax);
-        if (!__any_sync(0xffffffffu, over)) break;
-        raise(over);
+        lsum += part_sum;
+        tmem_st16(trow + kPart / 2 * cc, ph);
     }
-    lsum += step_sum;
-    tmem_st32(trow, *reinterpret_cast<uint32_t(*)[32]>(&ph[0]));
-    tmem_st32(trow + 32, *reinterpret_cast<uint32_t(*)[32]>(&ph[32]));
 }
 
 // A work item: the pair of q tiles `pair` (2 x 128 M rows) of KV head `kvh`
