@@ -167,11 +167,19 @@ def varlen_workspace_size(num_seqs: int, num_q_heads: int, num_kv_heads: int, he
     return n.value
 
 
-def _workspace(size_fn, workspace: Optional[torch.Tensor], device) -> torch.Tensor:
+def _empty(shape, dtype: torch.dtype, device, stream=None) -> torch.Tensor:
+    """A new tensor of the pool of the stream that the call runs on: memory is reused in that stream's order."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _workspace(size_fn, workspace: Optional[torch.Tensor], device, stream=None) -> torch.Tensor:
     """The caller's workspace as given (the library checks its size), or a new one."""
     if workspace is not None:
         return workspace
-    return torch.empty(max(size_fn(), 1), dtype=torch.uint8, device=device)
+    return _empty(max(size_fn(), 1), torch.uint8, device, stream)
 
 
 def attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Tensor,
@@ -197,7 +205,7 @@ def attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, b
         raise TypeError("q must have the cache dtype")
     B, hq, d = q.shape
     if out is None:
-        out = torch.empty((B, hq, d), dtype=out_dtype, device=q.device)
+        out = _empty((B, hq, d), out_dtype, q.device, stream)
     elif not out.is_contiguous() or out.shape != q.shape:
         raise ValueError("out must be contiguous [B, Hq, D]")
     if key_weights is not None:
@@ -207,7 +215,7 @@ def attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, b
             raise ValueError("q must be [B, Hq, D] with Hq a multiple of the cache's heads and its D")
         return _decode_weights("pkv_attn_decode_weights", c, q, block_tables, seq_lens, scale, window, key_weights, out,
                                workspace, err, stream)
-    ws = _workspace(lambda: decode_workspace_size(B, hq, c.num_kv_heads, d, q.device.index), workspace, q.device)
+    ws = _workspace(lambda: decode_workspace_size(B, hq, c.num_kv_heads, d, q.device.index), workspace, q.device, stream)
     mb = block_tables.shape[1] if block_tables.dim() == 2 else 0
     if (k_new is None) != (v_new is None):
         raise ValueError("k_new and v_new go together")
@@ -246,7 +254,7 @@ def _decode_weights(call: str, c, q, block_tables, seq_lens, scale, window, key_
     keys = block_tables.shape[1] * c.block_size
     seq_stride, head_stride = _key_weights(key_weights, B, c.num_kv_heads, keys)
     ws = _workspace(lambda: decode_workspace_size(B, hq, c.num_kv_heads, d, q.device.index, max_keys=keys), workspace,
-                    q.device)
+                    q.device, stream)
     check(getattr(lib(), call)(_ptr(q), _row_stride(q, "q") if B else hq * d, ctypes.byref(c), _ptr(block_tables), block_tables.shape[1],
                                _ptr(seq_lens), B, hq, float(scale), int(window), _ptr(key_weights), seq_stride,
                                head_stride, _ptr(out), _DT[out.dtype], _ptr(ws), ws.numel() * ws.element_size(),
@@ -274,8 +282,8 @@ def attn_varlen(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, b
     if cu_seqlens_q.numel() != B + 1:
         raise ValueError("cu_seqlens_q must have num_seqs + 1 entries")
     if out is None:
-        out = torch.empty((total, hq, d), dtype=out_dtype, device=q.device)
-    ws = _workspace(lambda: varlen_workspace_size(B, hq, c.num_kv_heads, d, q.device.index), workspace, q.device)
+        out = _empty((total, hq, d), out_dtype, q.device, stream)
+    ws = _workspace(lambda: varlen_workspace_size(B, hq, c.num_kv_heads, d, q.device.index), workspace, q.device, stream)
     if window > 0:
         check(lib().pkv_attn_varlen_window(_ptr(q), _row_stride(q, "q"), ctypes.byref(c), _ptr(block_tables),
                                            block_tables.shape[1], _ptr(cu_seqlens_q), _ptr(seq_lens), B, total,
@@ -336,13 +344,13 @@ def attn_decode_int8(q: torch.Tensor, kq: torch.Tensor, vq: torch.Tensor, k_scal
     _check_i32(seq_lens, "seq_lens")
     B, hq, d = q.shape
     if out is None:
-        out = torch.empty((B, hq, d), dtype=out_dtype, device=q.device)
+        out = _empty((B, hq, d), out_dtype, q.device, stream)
     if key_weights is not None:
         if hq % c.num_kv_heads or d != c.head_dim:
             raise ValueError("q must be [B, Hq, D] with Hq a multiple of the cache's heads and its D")
         return _decode_weights("pkv_attn_decode_int8_weights", c, q, block_tables, seq_lens, scale, window, key_weights,
                                out, workspace, err, stream)
-    ws = _workspace(lambda: decode_workspace_size(B, hq, c.num_kv_heads, d, q.device.index), workspace, q.device)
+    ws = _workspace(lambda: decode_workspace_size(B, hq, c.num_kv_heads, d, q.device.index), workspace, q.device, stream)
     check(lib().pkv_attn_decode_int8(_ptr(q), _row_stride(q, "q"), ctypes.byref(c), _ptr(block_tables),
                                      block_tables.shape[1], _ptr(seq_lens), B, hq, float(scale), int(window),
                                      _ptr(out), _DT[out.dtype], _ptr(ws), ws.numel() * ws.element_size(), _ptr(err),
@@ -371,10 +379,10 @@ def attn_varlen_int8(q: torch.Tensor, kq: torch.Tensor, vq: torch.Tensor, k_scal
         raise ValueError("q must be [total_q, Hq, D] with Hq a multiple of the cache's heads and its D")
     total, hq, d = q.shape
     if out is None:
-        out = torch.empty((total, hq, d), dtype=out_dtype, device=q.device)
+        out = _empty((total, hq, d), out_dtype, q.device, stream)
     if out.dtype not in _DT or not out.is_contiguous() or out.shape != q.shape:
         raise ValueError("out must be contiguous [total_q, Hq, D] of float32 or q's type")
-    ws = _workspace(lambda: varlen_workspace_size(B, hq, c.num_kv_heads, d, q.device.index), workspace, q.device)
+    ws = _workspace(lambda: varlen_workspace_size(B, hq, c.num_kv_heads, d, q.device.index), workspace, q.device, stream)
     check(lib().pkv_attn_varlen_int8(_ptr(q), _row_stride(q, "q") if total else hq * d, ctypes.byref(c), _ptr(block_tables),
                                      block_tables.shape[1], _ptr(cu_seqlens_q), _ptr(seq_lens), B, total, int(max_q_len),
                                      hq, float(scale), 1 if causal else 0, int(window), _ptr(out), _DT[out.dtype],
@@ -405,9 +413,9 @@ def evict_select(key_weights: torch.Tensor, seq_lens: torch.Tensor, budget: int,
         raise ValueError(f"seq_lens must have {B} entries and key_weights one KV head or more")
     seq_stride, head_stride = _key_weights(key_weights, B, hkv, keys)
     if kept is None:
-        kept = torch.empty((B, hkv, budget), dtype=torch.int32, device=key_weights.device)
+        kept = _empty((B, hkv, budget), torch.int32, key_weights.device, stream)
     if new_lens is None:
-        new_lens = torch.empty(B, dtype=torch.int32, device=key_weights.device)
+        new_lens = _empty(B, torch.int32, key_weights.device, stream)
     _check_i32(kept, "kept")
     _check_i32(new_lens, "new_lens")
     if kept.shape != (B, hkv, budget) or new_lens.numel() != B:

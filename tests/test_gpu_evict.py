@@ -595,3 +595,30 @@ def test_captured_and_replayed():
     for x, y in zip(*results):
         assert torch.equal(x.view(torch.int16) if x.dtype == torch.bfloat16 else x,
                            y.view(torch.int16) if y.dtype == torch.bfloat16 else y)
+
+
+def test_what_a_call_on_another_stream_allocates_is_not_reused_under_it():
+    """No workspace and no output given, a stream other than the current one with work queued on it: the current
+    stream takes and clears memory meanwhile."""
+    c = decode_case(41, [700, 90, 64, 1500], 16, 8, 128, 16, "f16", poison=False).to("cuda")
+    w = torch.zeros(4, 8, c.tables.shape[1] * 16, device="cuda")
+    want_w = w.clone()
+    args = (c.q, c.k_cache, c.v_cache, c.tables, c.lens, c.scale)
+    want = P.attn_decode(*args, key_weights=want_w)
+    want_kept, want_lens = P.evict_select(want_w, c.lens, 80, sink=4, recent=16)
+    size = P.decode_workspace_size(4, 16, 8, 128, max_keys=w.shape[2])
+    a, b = (torch.randn(4096, 4096, device="cuda") for _ in range(2))
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        for _ in range(40):                      # some tens of milliseconds
+            torch.mm(a, b, out=a)
+            a.clamp_(-1, 1)
+    out = P.attn_decode(*args, key_weights=w, stream=side)
+    kept, lens = P.evict_select(w, c.lens, 80, sink=4, recent=16, stream=side)
+    cleared = [torch.zeros(size, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    torch.cuda.synchronize()
+    assert len(cleared) == 4
+    assert torch.equal(out, want) and torch.equal(w, want_w)
+    assert torch.equal(kept, want_kept) and torch.equal(lens, want_lens)
